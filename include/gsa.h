@@ -290,6 +290,141 @@ GSA_API int gsa_special_attention_noalloc(const void *q_spec, const void *k_spec
  * GSA_ERR_CUDA if a CUDA call fails. */
 GSA_API int gsa_special_attention_noalloc_status(void *stream);
 
+/* ---- operators around the layer -------------------------------------------------
+ * Norms of queries and keys with the position rotation, a paged cache of keys
+ * and values, and attention of new tokens over that cache.  The pages describe
+ * no counterpart; they are what a program runs next to the layer: the layer's
+ * inputs are made from a projection, and frames that arrive one by one attend
+ * to the cached tokens of the earlier ones.  head_dim is 64 as in the layer.
+ *
+ * These calls create no context and allocate no memory: workspaces are the
+ * caller's, one per call in flight (two calls that overlap on the GPU, or two
+ * captured graphs that may run at the same time, need a workspace each).  All
+ * pointers are device pointers of the current device, 16-byte aligned; calls
+ * are asynchronous on `stream` and can be captured into a graph once one call
+ * on the device has run outside a capture.  Sizes and lengths that the host
+ * does not know (cu_tokens, lengths, block tables) are read on the device and
+ * checked there: what is out of range is left out and recorded, and
+ * gsa_operator_status reports it.
+ */
+#define GSA_NORM_NONE  0
+#define GSA_NORM_LAYER 1   /* (x - mean) / sqrt(var + eps) * weight + bias   */
+#define GSA_NORM_RMS   2   /* x / sqrt(mean(x^2) + eps) * weight             */
+
+/* Rows of 64 contiguous elements, one per (outer, token, head); strides in
+ * elements, multiples of 16 bytes, not negative.  Outer is the frame or the
+ * batch entry (unused, 0, where a call has tokens only). */
+typedef struct {
+    void *data;
+    int heads;
+    int64_t stride_outer, stride_token, stride_head;
+} gsa_rows;
+
+/* Norm over the 64 channels of each row, then the position rotation.
+ *   rope_axes 0  no rotation
+ *   rope_axes 1  channels (i, i + 32), i < 32, turn by p * base^(-i / 32)
+ *   rope_axes 2  channels 0..31 turn by the first coordinate, 32..63 by the
+ *                second: pairs (i, i + 16) of each half, angle p * base^(-i / 16)
+ * Angles are computed in 64 bits; norms and the rotation in fp32, rounded once. */
+typedef struct {
+    int dtype;          /* GSA_BF16 or GSA_FP32: rows, weights and biases       */
+    int norm;           /* GSA_NORM_*                                           */
+    float eps;
+    int rope_axes;      /* 0, 1 or 2                                            */
+    double rope_base;   /* > 0                                                  */
+} gsa_norm_rope;
+
+/* q_out = rotate(norm(q)), k_out = rotate(norm(k)), v_out = v, for
+ * n_outer x n_tokens tokens.  Each of q, k, v may be NULL with its output (left
+ * out); inputs and outputs have the same heads.  An output may be its own input
+ * (same pointer and strides); no other overlap.
+ *   q_weight, k_weight : [64], needed unless norm is GSA_NORM_NONE
+ *   q_bias, k_bias     : [64] or NULL; only with GSA_NORM_LAYER
+ *   positions          : int32 [n_tokens][rope_axes], outer entries
+ *                        pos_stride_outer ints apart (0: the same for all);
+ *                        NULL with rope_axes 0 */
+GSA_API int gsa_qk_norm_rope(const gsa_norm_rope *op, int64_t n_outer, int64_t n_tokens,
+                             const gsa_rows *q, const gsa_rows *k, const gsa_rows *v,
+                             const gsa_rows *q_out, const gsa_rows *k_out, const gsa_rows *v_out,
+                             const void *q_weight, const void *q_bias, const void *k_weight,
+                             const void *k_bias, const int32_t *positions,
+                             int64_t pos_stride_outer, void *stream);
+
+/* Gradients of gsa_qk_norm_rope: q and k are its inputs (op->dtype), d*_out the
+ * gradients of its outputs and d* those of its inputs, in grad_dtype (GSA_FP32,
+ * what gsa_backward writes, or GSA_BF16 where op->dtype is GSA_BF16 too).  Each
+ * of the three may be NULL with its gradients.  dq_weight, dq_bias, dk_weight,
+ * dk_bias: float32 [64], the sums over all rows, overwritten; NULL = not
+ * wanted.  The sums' order is fixed: equal calls give equal bits.  A gradient
+ * may be written over its own output gradient (same pointer and strides).
+ * workspace: gsa_qk_norm_rope_workspace_bytes() bytes, needed when a weight or
+ * bias gradient is wanted. */
+GSA_API int gsa_qk_norm_rope_backward(const gsa_norm_rope *op, int grad_dtype, int64_t n_outer, int64_t n_tokens,
+                                      const gsa_rows *q, const gsa_rows *k,
+                                      const gsa_rows *dq_out, const gsa_rows *dk_out, const gsa_rows *dv_out,
+                                      const gsa_rows *dq, const gsa_rows *dk, const gsa_rows *dv,
+                                      const void *q_weight, const void *k_weight, const int32_t *positions,
+                                      int64_t pos_stride_outer, float *dq_weight, float *dq_bias,
+                                      float *dk_weight, float *dk_bias, void *workspace,
+                                      size_t workspace_bytes, void *stream);
+GSA_API size_t gsa_qk_norm_rope_workspace_bytes(void);
+
+/* A paged cache: pools of pages and, per sequence, the pages that hold its
+ * tokens.  Token t of sequence b is row t % page_size of page
+ * block_table[b][t / page_size]; entries past a sequence's length are not read. */
+typedef struct {
+    void *k_pages, *v_pages;      /* [num_pages][kv_heads][page_size][64]             */
+    int dtype;                    /* GSA_BF16 or GSA_FP32                             */
+    int num_pages, page_size;     /* page_size 16, 32, 64, 128 or 256                 */
+    int kv_heads;
+    const int32_t *block_table;   /* [batch][max_pages], rows table_stride ints apart */
+    int batch, max_pages;
+    int64_t table_stride;
+} gsa_kv_cache;
+
+/* Write the keys (normed and rotated by `op`) and values of new tokens into the
+ * cache.  The tokens of sequence b are rows cu_tokens[b] .. cu_tokens[b + 1] - 1
+ * of k and v (n_tokens rows in all; rows from cu_tokens[batch] on are not
+ * used), and the first of them is token start[b] of the sequence.
+ *   cu_tokens : int32 [batch + 1], not decreasing;  start : int32 [batch]
+ *   positions : int32 [n_tokens][rope_axes]; NULL with rope_axes 0, and with
+ *               rope_axes 1 for a token's own place in its sequence
+ * A token whose place has no page in the table, or whose page is not one of the
+ * pool, is left out (GSA_ERR_DEVICE_BOUNDS from gsa_operator_status).  Two
+ * tokens with the same place leave either of the two in it. */
+GSA_API int gsa_cache_append(const gsa_kv_cache *cache, const gsa_norm_rope *op, int64_t n_tokens,
+                             const gsa_rows *k, const gsa_rows *v, const int32_t *cu_tokens,
+                             const int32_t *start, const void *k_weight, const void *k_bias,
+                             const int32_t *positions, void *stream);
+
+/* Attention of new tokens over the cache: query i of the n new tokens of
+ * sequence b attends to the sequence's cached tokens 0 .. lengths[b] - 1, or with
+ * `causal` to 0 .. lengths[b] - n + i (the new tokens are the last n cached ones).
+ * Query head h reads key head h / (q->heads / kv_heads); q->heads is a multiple
+ * of kv_heads.  Queries without a key give 0 (and lse -inf).
+ *   q, out    : rows of n_tokens tokens, cu_tokens as in gsa_cache_append; rows
+ *               from cu_tokens[batch] on are left as they are in out
+ *   lengths   : int32 [batch], the cached tokens of each sequence
+ *   max_new   : at least the most new tokens of a sequence (one that has more is
+ *               left out and recorded)
+ *   max_len   : about the longest of `lengths`; it only sets how the work is split
+ *   softmax_scale : 0 for 1 / 8
+ *   lse       : optional float32 [q heads][n_tokens], log-sum-exp of the scaled scores
+ *   workspace : gsa_cache_attention_workspace_bytes() of the same sizes
+ * Pages outside the pool are left out as if masked, and recorded.  Memory that no
+ * token stands in may hold anything.  A value that is not finite in a token of the
+ * sequence can reach every query of it, also those that do not see the token. */
+GSA_API int gsa_cache_attention(const gsa_kv_cache *cache, int64_t n_tokens, const gsa_rows *q,
+                                const gsa_rows *out, const int32_t *cu_tokens, const int32_t *lengths,
+                                int max_new, int64_t max_len, int causal, float softmax_scale, float *lse,
+                                void *workspace, size_t workspace_bytes, void *stream);
+GSA_API size_t gsa_cache_attention_workspace_bytes(const gsa_kv_cache *cache, int64_t n_tokens, int q_heads,
+                                                   int max_new, int64_t max_len);
+
+/* Status of the operators on the current device: synchronises `stream`, returns
+ * GSA_OK, GSA_ERR_DEVICE_BOUNDS or GSA_ERR_DEVICE_TIMEOUT and clears it. */
+GSA_API int gsa_operator_status(void *stream);
+
 #ifdef __cplusplus
 }
 #endif

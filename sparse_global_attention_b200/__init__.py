@@ -26,7 +26,9 @@ EXPORTED = ("gsa_create", "gsa_workspace_bytes", "gsa_forward", "gsa_dense_forwa
             "gsa_get_intermediate", "gsa_set_profiling", "gsa_get_kernel_times",
             "gsa_get_status", "gsa_strerror", "gsa_destroy", "gsa_special_attention_noalloc",
             "gsa_special_attention_noalloc_status",
-            "gsa_debug_expire_wait", "gsa_forward_host", "gsa_backward")
+            "gsa_debug_expire_wait", "gsa_forward_host", "gsa_backward", "gsa_qk_norm_rope",
+            "gsa_qk_norm_rope_backward", "gsa_qk_norm_rope_workspace_bytes", "gsa_cache_append",
+            "gsa_cache_attention", "gsa_cache_attention_workspace_bytes", "gsa_operator_status")
 
 
 class gsa_config(ctypes.Structure):
@@ -217,6 +219,7 @@ class GSALayer:
 
     def __init__(self, cfg: gsa_config):
         self.cfg = cfg
+        self._grid_pos = None          # default positions of split_qkv, made once
         self.ctx = gsa_create(cfg)
 
     @classmethod
@@ -298,6 +301,76 @@ class GSALayer:
                   p(gr["dv_img"]), p(gr["dw_g"]), st or None), "gsa_backward")
         return gr
 
+    def split_qkv(self, qkv, w_g, *, norm="layer", eps=1e-5, q_weight=None, q_bias=None, k_weight=None,
+                  k_bias=None, positions=None, rope_base=100.0, stream=None):
+        """The layer's inputs from a projection: qkv [frames, tokens, 3, heads, 64], per frame the special tokens then
+        the stored grid, queries and keys normed and rotated (qk_norm_rope) into the layer's layouts.
+
+        positions: int32 [tokens, axes] or [frames, tokens, axes]; default: special tokens at (0, 0), the token of grid
+        row y and column x at (y + 1, x + 1); False: no rotation.  Returns the dict that forward() takes."""
+        from . import operators
+        c, q, k, v, pos = self._qkv_parts(qkv, positions)
+        kw = dict(norm=norm, eps=eps, q_weight=q_weight, q_bias=q_bias, k_weight=k_weight, k_bias=k_bias,
+                  rope_base=rope_base, head_major=True, stream=stream)
+        ns, F, H = c.num_special, c.num_frames, c.num_heads
+        x = {"w_g": w_g}
+        cut = lambda t, s: None if t is None else t[..., s, :]
+        for name, at in (("spec", slice(0, ns)), ("img", slice(ns, None))):
+            shape = (H, F, ns, 64) if name == "spec" else (H, F, c.pad_h, c.pad_w, 64)
+            if name == "spec" and ns == 0:
+                got = [qkv.new_empty(shape)] * 3
+            else:
+                got = operators.qk_norm_rope(q[:, at], k[:, at], v[:, at], positions=cut(pos, at), **kw)
+            for a, t in zip("qkv", got):
+                x[f"{a}_{name}"] = t.view(shape)
+        return x
+
+    def split_qkv_backward(self, qkv, grads, *, norm="layer", eps=1e-5, q_weight=None, q_bias=None, k_weight=None,
+                           k_bias=None, positions=None, rope_base=100.0, stream=None):
+        """Gradients of split_qkv from those of the layer's inputs (backward()'s dict): float32 dqkv, shaped like qkv,
+        and dq_weight, dq_bias, dk_weight, dk_bias (None where there is none)."""
+        import torch
+        from . import operators
+        c, q, k, v, pos = self._qkv_parts(qkv, positions)
+        kw = dict(norm=norm, eps=eps, q_weight=q_weight, q_bias=q_bias, k_weight=k_weight, k_bias=k_bias,
+                  rope_base=rope_base, head_major=True, stream=stream)
+        ns, F, H = c.num_special, c.num_frames, c.num_heads
+        cut = lambda t, s: None if t is None else t[..., s, :]
+        with operators._On(qkv.device, stream):
+            d = torch.empty(qkv.shape, dtype=torch.float32, device=qkv.device)
+            res = {"dqkv": d}
+            for name, at in (("spec", slice(0, ns)), ("img", slice(ns, None))):
+                if name == "spec" and ns == 0:
+                    continue
+                g = [grads[f"d{a}_{name}"].reshape(H, F, -1, 64) for a in "qkv"]
+                r = operators.qk_norm_rope_backward(q[:, at], k[:, at], *g, positions=cut(pos, at),
+                                                    out=[d[:, at, i] for i in range(3)], **kw)
+                for n in ("dq_weight", "dq_bias", "dk_weight", "dk_bias"):
+                    res[n] = r[n] if res.get(n) is None else res[n] + r[n]
+        return res
+
+    def _qkv_parts(self, qkv, positions):
+        import torch
+        c = self.cfg
+        tokens = c.num_special + c.pad_h * c.pad_w
+        if not qkv.is_cuda or tuple(qkv.shape) != (c.num_frames, tokens, 3, c.num_heads, 64):
+            raise GSAError(f"qkv must be a CUDA tensor [{c.num_frames}, {tokens}, 3, {c.num_heads}, 64], "
+                           f"got {tuple(qkv.shape)} on {qkv.device}")
+        if qkv.dtype != (torch.bfloat16 if c.dtype == GSA_BF16 else torch.float32):
+            raise GSAError(f"qkv must have the layer's type, got {qkv.dtype}")
+        if positions is None:
+            if self._grid_pos is None or self._grid_pos.device != qkv.device:
+                at = torch.arange(c.pad_h * c.pad_w, dtype=torch.int32)
+                grid = torch.stack([at // c.pad_w + 1, at % c.pad_w + 1], dim=1).to(torch.int32)
+                pos = torch.cat([torch.zeros(c.num_special, 2, dtype=torch.int32), grid])
+                self._grid_pos = pos.to(qkv.device)
+                # ready for calls on any stream from here on
+                torch.cuda.current_stream(qkv.device).synchronize()
+            positions = self._grid_pos
+        elif positions is False:
+            positions = None
+        return c, qkv[:, :, 0], qkv[:, :, 1], qkv[:, :, 2], positions
+
     def dense(self, q, k, v, o=None, stream=None):
         import torch
         o = torch.empty_like(q) if o is None else o
@@ -335,3 +408,15 @@ def _raw_u8(ptr: int, nbytes: int):
         __cuda_array_interface__ = {"shape": (nbytes,), "typestr": "|u1", "data": (ptr, False),
                                     "version": 3, "strides": None}
     return torch.as_tensor(_Holder(), device="cuda")
+
+
+# operators around the layer (torch is imported with the first use of one)
+OPERATORS = ("qk_norm_rope", "qk_norm_rope_backward", "KVCache", "operator_status")
+
+
+def __getattr__(name):
+    if name in OPERATORS:
+        from . import operators
+        globals().update({n: getattr(operators, n) for n in OPERATORS})
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
