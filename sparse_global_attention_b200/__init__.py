@@ -336,17 +336,19 @@ class GSALayer:
                   rope_base=rope_base, head_major=True, stream=stream)
         ns, F, H = c.num_special, c.num_frames, c.num_heads
         cut = lambda t, s: None if t is None else t[..., s, :]
-        with operators._On(qkv.device, stream):
-            d = torch.empty(qkv.shape, dtype=torch.float32, device=qkv.device)
-            res = {"dqkv": d}
-            for name, at in (("spec", slice(0, ns)), ("img", slice(ns, None))):
-                if name == "spec" and ns == 0:
-                    continue
-                g = [grads[f"d{a}_{name}"].reshape(H, F, -1, 64) for a in "qkv"]
-                r = operators.qk_norm_rope_backward(q[:, at], k[:, at], *g, positions=cut(pos, at),
-                                                    out=[d[:, at, i] for i in range(3)], **kw)
-                for n in ("dq_weight", "dq_bias", "dk_weight", "dk_bias"):
-                    res[n] = r[n] if res.get(n) is None else res[n] + r[n]
+        if stream is not None:
+            return operators._elsewhere(qkv.device, stream, self.split_qkv_backward, qkv, grads, positions=positions,
+                                        **{n: kw[n] for n in kw if n not in ("head_major", "stream")})
+        d = torch.empty(qkv.shape, dtype=torch.float32, device=qkv.device)
+        res = {"dqkv": d}
+        for name, at in (("spec", slice(0, ns)), ("img", slice(ns, None))):
+            if name == "spec" and ns == 0:
+                continue
+            g = [grads[f"d{a}_{name}"].reshape(H, F, -1, 64) for a in "qkv"]
+            r = operators.qk_norm_rope_backward(q[:, at], k[:, at], *g, positions=cut(pos, at),
+                                                out=[d[:, at, i] for i in range(3)], **kw)
+            for n in ("dq_weight", "dq_bias", "dk_weight", "dk_bias"):
+                res[n] = r[n] if res.get(n) is None else res[n] + r[n]
         return res
 
     def _qkv_parts(self, qkv, positions):
