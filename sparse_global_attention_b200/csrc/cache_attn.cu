@@ -9,16 +9,24 @@
 //
 // bf16 runs on the tensor cores (tcgen05, TMEM accumulators, K/V pages by TMA,
 // one box per page and tile): S = Q K^T from shared memory, P in TMEM, O += P V.
-// Warp roles: softmax warps (thread = row = TMEM lane), one TMA producer, one MMA
-// issuer.  Variants by the rows of a sequence and key head:
-//   two tiles of 128 rows per block (a chunk of tokens): every key tile that
-//     arrives serves 256 rows, and one tile's exponentials run while the other's
-//     products do;
-//   one tile of 128 rows, two blocks per SM (a few tokens);
-//   at most 32 rows (single tokens): the rows are repeated in the four 32-lane
-//     quarters of TMEM and each of the four softmax warps takes 32 of a tile's 128
-//     keys for all rows (its P is zero elsewhere), so no warp does four times the
-//     exponentials; the quarters' sums are joined at the end.
+// A stream is 128 rows with S, P and O in TMEM and its softmax warps (thread = row = TMEM
+// lane; two warps share 32 rows, 64 keys of a tile each); a block keeps two streams, one
+// TMA producer and one MMA issuer.  What bounds a chunk of tokens is the softmax: at 64
+// channels a tile's exponentials (16 results per clock and SM) take twice as long as its
+// products.  Two streams let one's exponentials run beside the other's waits; the issuer's
+// fixed order (S and P V of one stream, then of the other) keeps them out of step, which an
+// issuer for each stream did not (1183 against 977 us, 1301 queries of 16 heads over 83,264
+// keys, one block per 256 rows), nor turns taken by barriers (1000), three streams
+// of 64-key tiles (1404), or reading the next scores under the exponentials (1464).  3 of
+// 16 exponentials run on the FMA pipe (913 against 924 us; 4 of 16: 961).
+// Variants by the rows of a sequence and key head:
+//   ROW_TILES (a chunk of tokens): the streams are two row tiles over the same keys;
+//   ONE_TILE (up to 128 rows): the streams take every other tile of the keys for the same
+//     rows, and their sums are joined at the end;
+//   QUARTERS (up to 32 rows, single tokens): one stream of 128-key tiles, two blocks per
+//     SM; the rows are repeated in the four 32-lane quarters of TMEM and each softmax
+//     warp takes 32 of a tile's keys for all of them (its P is zero elsewhere), so no
+//     warp does four times the exponentials.
 // Rows of V that no key stands for (the cache's memory behind a sequence's last
 // token, pages that do not exist) are zeroed in shared memory before the product,
 // since 0 * NaN is NaN; scores of such keys are replaced, not added to.
@@ -27,8 +35,10 @@
 //
 // All mbarrier waits are bounded; one that runs out records GSA_ERR_DEVICE_TIMEOUT.
 #include <atomic>
+#include <math.h>
 #include <cuda.h>
 #include <string.h>
+#include <type_traits>
 
 #include "operators.h"
 #include "tc_ptx.cuh"
@@ -40,37 +50,47 @@ namespace {
 
 using namespace tc;
 
-constexpr int TM = 128;                  // rows per tensor-core tile
-constexpr int TN = 128;                  // keys per tile
-constexpr int TILE = TN * 128;           // bytes of one 128 x 64 bf16 tile
+constexpr int TM = 128;                  // rows of a tile
+constexpr int QTILE = TM * 128;          // bytes of 128 rows of 64 bf16
 constexpr float RESCALE_LOG2 = 8.f;      // rescale O when the max grows by > 2^8
-constexpr uint32_t IDESC_QK = idesc_bf16(128, 128, false);
-constexpr uint32_t IDESC_PV = idesc_bf16(128, 64, true);
+constexpr int FMA_PAIRS = 3;              // of 16 pairs of a tile's exponentials, on the FMA pipe
 constexpr float LN2 = 0.6931471805599453f;
-
 // kernel variants
-enum Kind : int { TWO_TILES = 0, ONE_TILE = 1, QUARTERS = 2, F32_64 = 3, F32_16 = 4 };
+enum Kind : int { ROW_TILES = 0, ONE_TILE = 1, QUARTERS = 2, F32_64 = 3, F32_16 = 4 };
 
 template <int KIND>
 struct Lay {
-  static constexpr int NQ = KIND == TWO_TILES ? 2 : 1;
-  static constexpr int NST = KIND == TWO_TILES ? 5 : 3;      // K/V ring depth
-  static constexpr int ROWS = KIND == QUARTERS ? 32 : NQ * TM;
-  static constexpr int NWARP = 4 * NQ;                       // softmax warps
+  static constexpr bool QUAD = KIND == QUARTERS;
+  static constexpr int NS = QUAD ? 1 : 2;                    // streams: four softmax warps and an MMA issuer each
+  static constexpr int R = KIND == ROW_TILES ? 2 : 1;        // row tiles; with one, stream s takes tiles s, s + NS, ..
+  static constexpr int STEP = KIND == ONE_TILE ? NS : 1;
+  static constexpr int ROWS = QUAD ? 32 : R * TM;
+  static constexpr int TK = 128;                             // keys per tile
+  static constexpr int NST = QUAD ? 3 : (R == 2 ? 5 : 6);    // K/V ring depth
+  static constexpr int HALVES = QUAD ? 1 : 2;                // softmax warps that share 32 rows, 64 keys of a tile each
+  static constexpr int TWARP = 4 * HALVES;                   // softmax warps of a stream
+  static constexpr int NWARP = TWARP * NS;                   // then the producer and the issuer
   static constexpr int NTHREADS = 32 * (NWARP + 2);
-  static constexpr int COLS = KIND == TWO_TILES ? 512 : 256; // TMEM columns
-  static constexpr int TO = 128 * NQ, TP = TO + 64 * NQ;     // S_i at 128 i, O_i and P_i after
-  static constexpr int KV = NQ * TILE;
+  static constexpr int COLS = QUAD ? 256 : 512;              // TMEM columns: S, O and P of each stream
+  static constexpr int TO = TK * NS, TP = TO + 64 * NS;
+  static constexpr int TILE = TK * 128;                      // bytes of a tile of K or V
+  static constexpr int KV = R * QTILE;
   static constexpr int STAGE = 2 * TILE;
   static constexpr int BAR = KV + NST * STAGE;
-  // q_full, full[NST], empty[NST], s_full[NQ], s_free[NQ], p_full[NQ], pv_done[NQ], fin
-  static constexpr int NBAR = 2 + 2 * NST + 4 * NQ;
+  // q_full, full[NST], empty[NST], then s_full, s_free, p_full, pv_done of each stream, fin
+  static constexpr int NBAR = 2 + 2 * NST + 4 * NS;
   static constexpr int INFO = BAR + NBAR * 8;                // valid boxes of each stage, "some are not"
   static constexpr int SLOT = INFO + 4 * (NST + 1);
-  static constexpr int BYTES = SLOT + 16;
+  static constexpr int XCH = (SLOT + 4 + 15) / 16 * 16;      // one float per row between two halves
+  static constexpr int BYTES = XCH + (HALVES == 2 ? 4 * TM * NS : 0);
+  static constexpr uint32_t IDESC_QK = idesc_bf16(128, TK, false);
+  static constexpr uint32_t IDESC_PV = idesc_bf16(128, 64, true);
 };
 static_assert(2 * (Lay<QUARTERS>::BYTES + 1024) <= 228 * 1024, "two blocks per SM");
-static_assert(4 * 32 * 66 * 4 <= Lay<QUARTERS>::NST * Lay<QUARTERS>::STAGE, "the quarters' sums fit the ring");
+static_assert(Lay<ROW_TILES>::BYTES <= 227 * 1024 && Lay<ONE_TILE>::BYTES <= 227 * 1024, "one block per SM");
+constexpr int PITCH = 66;                // floats of a row's part (64 sums, max, sum) in shared memory
+static_assert(4 * 32 * PITCH * 4 <= Lay<QUARTERS>::NST * Lay<QUARTERS>::STAGE, "the quarters' parts fit the ring");
+static_assert(TM * PITCH * 4 <= Lay<ONE_TILE>::NST * Lay<ONE_TILE>::STAGE, "a stream's part fits the ring");
 
 template <int KIND>
 struct Bars {
@@ -79,12 +99,98 @@ struct Bars {
   __device__ uint32_t q_full() const { return base; }
   __device__ uint32_t full(int s) const { return base + 8 * (1 + s); }
   __device__ uint32_t empty(int s) const { return base + 8 * (1 + L::NST + s); }
-  __device__ uint32_t s_full(int i) const { return base + 8 * (1 + 2 * L::NST + i); }
-  __device__ uint32_t s_free(int i) const { return base + 8 * (1 + 2 * L::NST + L::NQ + i); }
-  __device__ uint32_t p_full(int i) const { return base + 8 * (1 + 2 * L::NST + 2 * L::NQ + i); }
-  __device__ uint32_t pv_done(int i) const { return base + 8 * (1 + 2 * L::NST + 3 * L::NQ + i); }
-  __device__ uint32_t fin() const { return base + 8 * (1 + 2 * L::NST + 4 * L::NQ); }
+  __device__ uint32_t s_full(int i) const { return base + 8 * (1 + 2 * L::NST + 4 * i); }
+  __device__ uint32_t s_free(int i) const { return base + 8 * (2 + 2 * L::NST + 4 * i); }
+  __device__ uint32_t p_full(int i) const { return base + 8 * (3 + 2 * L::NST + 4 * i); }
+  __device__ uint32_t pv_done(int i) const { return base + 8 * (4 + 2 * L::NST + 4 * i); }
+  __device__ uint32_t fin() const { return base + 8 * (1 + 2 * L::NST + 4 * L::NS); }
 };
+
+// whether any of the 64 threads of two warps says so (and a barrier between them)
+__device__ __forceinline__ bool pair_any(int id, bool p) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %2, 0;\n barrier.cta.red.or.pred q, %1, 64, p;\n"
+      " selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(r)
+      : "r"(id), "r"(static_cast<uint32_t>(p))
+      : "memory");
+  return r != 0;
+}
+
+// a warp's bounded wait: true if the phase is complete for all its lanes
+__device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, int* err) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p, q;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " vote.sync.all.pred q, p, 0xffffffff;\n selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  if (ok) return true;
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, err));
+}
+
+// values that an asynchronous load has written by now: nothing reads them earlier
+template <int N>
+__device__ __forceinline__ void tie(uint32_t* v) {
+#pragma unroll
+  for (int e = 0; e < N; ++e) asm volatile("" : "+r"(v[e]));
+}
+
+// the largest of N values, three at a time, in four chains
+__device__ __forceinline__ float max3(float a, uint32_t b, uint32_t c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;\n" : "=f"(d) : "f"(a), "f"(__uint_as_float(b)), "f"(__uint_as_float(c)));
+  return d;
+}
+template <int N>
+__device__ __forceinline__ float row_max(const uint32_t* v) {
+  float m[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) m[k] = fmaxf(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1]));
+#pragma unroll
+  for (int e = 8; e < N; e += 8)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) m[k] = max3(m[k], v[e + 2 * k], v[e + 2 * k + 1]);
+  return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+}
+
+// Two exponentials on the FMA and integer pipes instead of the exponential unit
+// (16 results per clock and SM, what bounds a chunk of tokens): 2^x = 2^n 2^r with n
+// the nearest integer, r in [-1/2, 1/2] (Cody and Waite's reduction, exact here), 2^r by
+// the degree-4 polynomial of least relative error (2.6e-6 = 2^-18.6, fitted by Remez'
+// exchange; bf16 weights keep 2^-8, their fp32 sum 2^-18).  Adding 1.5 * 2^23 + 127 leaves
+// n + 127 in the low bits, so one shift gives the float 2^n.  x is held above -126 (2^-126
+// instead of less, or of 0 for -inf: only unmasked tiles come here); NaN stays NaN.
+__device__ __forceinline__ void exp2_pair_fma(uint32_t s0, uint32_t s1, float sl2, float nmb, float& l0, float& l1,
+                                              float& p0, float& p1) {
+  float x0, x1;
+  asm("{\n .reg .b64 a, b, c, d;\n"
+      " mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %4};\n mov.b64 c, {%5, %5};\n"
+      " fma.rn.f32x2 d, a, b, c;\n mov.b64 {%0, %1}, d;\n}\n"
+      : "=f"(x0), "=f"(x1)
+      : "r"(s0), "r"(s1), "f"(sl2), "f"(nmb));
+  asm("max.NaN.f32 %0, %0, 0fC2FC0000;\n" : "+f"(x0));      // -126
+  asm("max.NaN.f32 %0, %0, 0fC2FC0000;\n" : "+f"(x1));
+  constexpr float MAGIC = 12583039.f;                       // 1.5 * 2^23 + 127
+  asm("{\n .reg .b64 x, t, r, p, c, m;\n .reg .b32 t0, t1;\n"
+      " mov.b64 x, {%0, %1};\n mov.b64 m, {%4, %4};\n add.rn.f32x2 t, x, m;\n"
+      " mov.b64 m, {%5, %5};\n add.rn.f32x2 r, t, m;\n"
+      " mov.b64 m, {%6, %6};\n fma.rn.f32x2 r, r, m, x;\n"
+      " mov.b64 p, {%7, %7};\n mov.b64 c, {%8, %8};\n fma.rn.f32x2 p, p, r, c;\n"
+      " mov.b64 c, {%9, %9};\n fma.rn.f32x2 p, p, r, c;\n"
+      " mov.b64 c, {%10, %10};\n fma.rn.f32x2 p, p, r, c;\n"
+      " mov.b64 c, {%11, %11};\n fma.rn.f32x2 p, p, r, c;\n"
+      " mov.b64 {t0, t1}, t;\n shl.b32 t0, t0, 23;\n shl.b32 t1, t1, 23;\n mov.b64 t, {t0, t1};\n"
+      " mul.rn.f32x2 p, p, t;\n mov.b64 {%0, %1}, p;\n"
+      " mov.b64 c, {%2, %3};\n add.rn.f32x2 c, c, p;\n mov.b64 {%2, %3}, c;\n}\n"
+      : "+f"(x0), "+f"(x1), "+f"(l0), "+f"(l1)
+      : "f"(MAGIC), "f"(-MAGIC), "f"(-1.f), "f"(0.009570102207362652f), "f"(0.05591785907745361f),
+        "f"(0.240247443318367f), "f"(0.6931217908859253f), "f"(0.9999992847442627f));
+  p0 = x0;
+  p1 = x1;
+}
 
 // where a block's work lies: one tile of rows of one sequence and key head, and
 // one split of its key tiles
@@ -103,10 +209,11 @@ __device__ __forceinline__ Block block_of(const CacheAttnArgs& a) {
   unsigned x = blockIdx.x;
   k.split = x % a.n_split;
   x /= a.n_split;
-  const int tile = a.row_tiles - 1 - static_cast<int>(x % a.row_tiles);   // causal: the longest first
-  x /= a.row_tiles;
   k.h = x % a.c.heads;
-  k.b = x / a.c.heads;
+  x /= a.c.heads;
+  k.b = x % a.c.batch;
+  // with a causal mask a sequence's last tile has the most keys: it starts first
+  const int tile = a.causal ? a.row_tiles - 1 - static_cast<int>(x / a.c.batch) : static_cast<int>(x / a.c.batch);
   k.seq = sequence_of(a, k.b);
   const long long room = static_cast<long long>(a.c.max_pages) << a.c.page_shift;
   k.len = static_cast<int>(min(static_cast<long long>(k.seq.len), room));
@@ -137,11 +244,37 @@ __device__ __forceinline__ int page_of(const CacheAttnArgs& a, int raw) {
   return raw >= 0 && raw < a.c.num_pages ? raw : -1;
 }
 
+// a row's result: normalised output and log-sum-exp, or this split's part
+template <int N>
+__device__ __forceinline__ void write_row(const CacheAttnArgs& a, const Block& blk, int at, int head, int e0,
+                                          const float (&o)[N], float m, float l) {
+  if (a.n_split == 1) {
+    const float inv = l > 0.f ? 1.f / l : (l == l ? 0.f : l);        // a NaN stays one
+    __nv_bfloat16* d = static_cast<__nv_bfloat16*>(a.out.p) + at * a.out.st + head * a.out.sh + e0;
+#pragma unroll
+    for (int e = 0; e < N; e += 8)
+      *reinterpret_cast<uint4*>(d + e) =
+          make_uint4(pack_bf16(o[e] * inv, o[e + 1] * inv), pack_bf16(o[e + 2] * inv, o[e + 3] * inv),
+                     pack_bf16(o[e + 4] * inv, o[e + 5] * inv), pack_bf16(o[e + 6] * inv, o[e + 7] * inv));
+    if (a.lse && e0 == 0)
+      a.lse[static_cast<long long>(head) * a.n_tokens + at] = l == 0.f ? -INFINITY : (m * a.scale_log2 + log2f(l)) * LN2;
+  } else {
+    const long long pr = (static_cast<long long>(blk.split) * a.n_tokens + at) * a.q.heads + head;
+    if (blk.ntile > 0) {
+#pragma unroll
+      for (int e = 0; e < N; e += 4)
+        *reinterpret_cast<float4*>(a.part_o + pr * D + e0 + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+    }
+    if (e0 == 0) *reinterpret_cast<float2*>(a.part_ml + pr * 2) = make_float2(m, l);
+  }
+}
+
 template <int KIND>
-__global__ void __launch_bounds__(Lay<KIND>::NTHREADS, KIND == TWO_TILES ? 1 : 2)
+__global__ void __launch_bounds__(Lay<KIND>::NTHREADS, KIND == QUARTERS ? 2 : 1)
     cache_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                       const __grid_constant__ CacheAttnArgs a) {
   using L = Lay<KIND>;
+  constexpr int TN = L::TK;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);          // 1024-byte aligned: no static shared memory before it
   const Bars<KIND> bars{sbase + L::BAR};
@@ -155,20 +288,21 @@ __global__ void __launch_bounds__(Lay<KIND>::NTHREADS, KIND == TWO_TILES ? 1 : 2
     if (threadIdx.x == 0) set_error(a.err, ERR_BOUNDS);
     return;
   }
-  const int nq = (L::NQ == 2 && blk.rows - blk.row0 > TM) ? 2 : 1;      // tiles that hold rows
   const int ntile = blk.ntile;
+  const int nrow = min(L::R, (blk.rows - blk.row0 + TM - 1) / TM);   // row tiles that hold rows
+  const int nstream = L::R > 1 ? nrow : L::NS;
   int* err = a.err + 1;
 
   if (threadIdx.x == 0) {
-    mbar_init(bars.q_full(), 4 * nq);
+    mbar_init(bars.q_full(), L::TWARP * nrow);
     for (int s = 0; s < L::NST; ++s) {
       mbar_init(bars.full(s), 1);
       mbar_init(bars.empty(s), 1);
     }
-    for (int i = 0; i < L::NQ; ++i) {
+    for (int i = 0; i < L::NS; ++i) {
       mbar_init(bars.s_full(i), 1);
-      mbar_init(bars.s_free(i), 4);              // one arrival per softmax warp
-      mbar_init(bars.p_full(i), 4);
+      mbar_init(bars.s_free(i), L::TWARP);       // one arrival per softmax warp
+      mbar_init(bars.p_full(i), L::TWARP);
       mbar_init(bars.pv_done(i), 1);
     }
     mbar_init(bars.fin(), 1);
@@ -183,151 +317,156 @@ __global__ void __launch_bounds__(Lay<KIND>::NTHREADS, KIND == TWO_TILES ? 1 : 2
 
   const int page_size = 1 << a.c.page_shift;
   const int box = min(page_size, TN);             // rows of one copy
-  const int box_shift = min(a.c.page_shift, 7);
+  const int box_shift = min(a.c.page_shift, TN == 128 ? 7 : 6);
   const int nbox = TN >> box_shift;
 
   if (warp == L::NWARP) {
     // ------------------------------------------------------------ TMA producer
     // lanes 0-7 copy the tile's boxes of K, lanes 8-15 those of V
-    if (ntile > 0) {
-      const int* table = a.c.table + blk.b * a.c.table_stride;
-      const int my = lane & 7;
-      const bool mine = lane < 16 && my < nbox;
-      auto slot_of = [&](int it) { return (blk.t_begin + it) * TN + (my << box_shift); };
-      auto lookup = [&](int it) {
-        const int slot = slot_of(it);
-        return mine && it < ntile && slot < blk.len ? table[slot >> a.c.page_shift] : -1;
-      };
-      int next = lookup(0);
-      int issued = 0;
-      for (int it = 0; it < ntile; ++it) {
-        const int s = it % L::NST;
-        const int raw = next;
-        next = lookup(it + 1);
-        if (it >= L::NST &&
-            !__all_sync(0xffffffffu, mbar_wait(bars.empty(s), ((it / L::NST) - 1) & 1, err)))
-          break;
-        const int slot = slot_of(it);
-        const bool want = mine && slot < blk.len;
-        const int page = want ? page_of(a, raw) : -1;
-        const uint32_t good = __ballot_sync(0xffffffffu, page >= 0);
-        if (__any_sync(0xffffffffu, want && page < 0) && lane == 0) {
-          set_error(a.err, ERR_BOUNDS);
-          info[L::NST] = 1;
-        }
-        if (lane == 0) {
-          info[s] = good & 0xffu;
-          mbar_expect_tx(bars.full(s), __popc(good) * box * 128);
-        }
-        __syncwarp();
-        if (page >= 0) {
-          const int y = ((page * a.c.heads + blk.h) << a.c.page_shift) + (slot & (page_size - 1));
-          const uint32_t dst = sbase + L::KV + s * L::STAGE + (lane >= 8 ? TILE : 0) + (my << box_shift) * 128;
-          tma_load_2d(dst, lane >= 8 ? &tm_v : &tm_k, 0, y, bars.full(s));
-        }
-        __syncwarp();
-        ++issued;
+    const int* table = a.c.table + blk.b * a.c.table_stride;
+    const int my = lane & 7;
+    const bool mine = lane < 16 && my < nbox;
+    auto slot_of = [&](int it) { return (blk.t_begin + it) * TN + (my << box_shift); };
+    auto lookup = [&](int it) {
+      const int slot = slot_of(it);
+      return mine && it < ntile && slot < blk.len ? table[slot >> a.c.page_shift] : -1;
+    };
+    int next = lookup(0);
+    int issued = 0;
+    for (int it = 0; it < ntile; ++it) {
+      const int s = it % L::NST;
+      const int raw = next;
+      next = lookup(it + 1);
+      if (it >= L::NST && !wait_all(bars.empty(s), ((it / L::NST) - 1) & 1, err)) break;
+      const int slot = slot_of(it);
+      const bool want = mine && slot < blk.len;
+      const int page = want ? page_of(a, raw) : -1;
+      const uint32_t good = __ballot_sync(0xffffffffu, page >= 0);
+      if (__any_sync(0xffffffffu, want && page < 0) && lane == 0) {
+        set_error(a.err, ERR_BOUNDS);
+        info[L::NST] = 1;
       }
-      // drain: every issued copy has landed before the block may exit
-      for (int it = max(0, issued - L::NST); it < issued; ++it)
-        mbar_wait(bars.full(it % L::NST), (it / L::NST) & 1, err);
+      if (lane == 0) {
+        info[s] = good & 0xffu;
+        mbar_expect_tx(bars.full(s), __popc(good) * box * 128);
+      }
+      __syncwarp();
+      if (page >= 0) {
+        const int y = ((page * a.c.heads + blk.h) << a.c.page_shift) + (slot & (page_size - 1));
+        const uint32_t dst = sbase + L::KV + s * L::STAGE + (lane >= 8 ? L::TILE : 0) + (my << box_shift) * 128;
+        tma_load_2d(dst, lane >= 8 ? &tm_v : &tm_k, 0, y, bars.full(s));
+      }
+      __syncwarp();
+      ++issued;
     }
+    // drain: every issued copy has landed before the block may exit
+    for (int it = max(0, issued - L::NST); it < issued; ++it)
+      mbar_wait(bars.full(it % L::NST), (it / L::NST) & 1, err);
   } else if (warp == L::NWARP + 1) {
     // ------------------------------------------------------------ MMA issuer
+    // Stream i's n-th tile is j = first_i + n * STEP.  S of tile n and then O += P V of tile n - 1,
+    // stream after stream: the fixed order keeps the streams' softmax out of step.
     if (ntile > 0) {
       const bool leader = elect_one();
       const uint64_t dq0 = sdesc_sw128(sbase, 16, 1024);
       const uint64_t dk0 = sdesc_sw128(sbase + L::KV, 16, 1024);
-      const uint64_t dv0 = sdesc_sw128(sbase + L::KV + TILE, 8192, 1024);
-      constexpr uint32_t T16 = TILE >> 4, ST16 = L::STAGE >> 4;
-      bool ok = __all_sync(0xffffffffu, mbar_wait(bars.q_full(), 0, err));
-      tc_fence_after();
-      for (int j = 0; ok && j <= ntile; ++j) {
-        if (j < ntile) {
-          const int s = j % L::NST;
-          ok = __all_sync(0xffffffffu, mbar_wait(bars.full(s), (j / L::NST) & 1, err));
-          if (!ok) break;
-          const int kb = (blk.t_begin + j) * TN;
-          const uint32_t bits = info[s];
-          if (kb + TN > blk.len || bits != (1u << nbox) - 1u) {
-            // rows of V without a key
-            for (int r = lane; r < TN; r += 32)
-              if (kb + r >= blk.len || !((bits >> (r >> box_shift)) & 1u)) {
-                uint4* p = reinterpret_cast<uint4*>(smem + L::KV + s * L::STAGE + TILE + r * 128);
-#pragma unroll
-                for (int c = 0; c < 8; ++c) p[c] = make_uint4(0, 0, 0, 0);
-              }
-            fence_async_smem();
-            __syncwarp();
-          }
-          tc_fence_after();
-        }
-        const uint64_t dk = dk0 + (j % L::NST) * ST16;
-        const uint64_t dv = dv0 + ((j + L::NST - 1) % L::NST) * ST16;
-        for (int i = 0; i < nq && ok; ++i) {
+      const uint64_t dv0 = sdesc_sw128(sbase + L::KV + L::TILE, 8192, 1024);
+      constexpr uint32_t ST16 = L::STAGE >> 4;
+      const int most = (ntile + L::STEP - 1) / L::STEP;
+      bool ok = wait_all(bars.q_full(), 0, err);
+      for (int n = 0; ok && n <= most; ++n) {
+        for (int i = 0; i < nstream; ++i) {
+          const int j = (L::R > 1 ? 0 : i) + n * L::STEP, s = j % L::NST;
           if (j < ntile) {
-            // S_i = Q_i K_j^T as soon as the softmax warps hold S_i of tile j - 1
-            if (j > 0) {
-              ok = __all_sync(0xffffffffu, mbar_wait(bars.s_free(i), (j - 1) & 1, err));
+            if (L::R == 1 || i == 0) {
+              ok = wait_all(bars.full(s), (j / L::NST) & 1, err);
               if (!ok) break;
-              tc_fence_after();
+              const int kb = (blk.t_begin + j) * TN;
+              const uint32_t bits = info[s];
+              if (kb + TN > blk.len || bits != (1u << nbox) - 1u) {
+                // rows of V without a key
+                for (int r = lane; r < TN; r += 32)
+                  if (kb + r >= blk.len || !((bits >> (r >> box_shift)) & 1u)) {
+                    uint4* p = reinterpret_cast<uint4*>(smem + L::KV + s * L::STAGE + L::TILE + r * 128);
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) p[c] = make_uint4(0, 0, 0, 0);
+                  }
+                fence_async_smem();
+                __syncwarp();
+              }
             }
+            // S = Q K^T as soon as the softmax warps hold S of tile n - 1
+            if (n > 0) {
+              ok = wait_all(bars.s_free(i), (n - 1) & 1, err);
+              if (!ok) break;
+            }
+            tc_fence_after();
             if (leader) {
+              const uint64_t dq = dq0 + (L::R > 1 ? i : 0) * (QTILE >> 4), dk = dk0 + s * ST16;
 #pragma unroll
               for (int ks = 0; ks < 4; ++ks)
-                mma_bf16_ss(tmem + 128 * i, dq0 + i * T16 + 2 * ks, dk + 2 * ks, IDESC_QK, ks > 0 ? 1u : 0u);
+                mma_bf16_ss(tmem + TN * i, dq + 2 * ks, dk + 2 * ks, L::IDESC_QK, ks > 0 ? 1u : 0u);
               mma_commit(bars.s_full(i));
             }
             __syncwarp();
           }
-          if (j > 0) {
-            // O_i += P_i V_{j-1}
-            ok = __all_sync(0xffffffffu, mbar_wait(bars.p_full(i), (j - 1) & 1, err));
+          const int jp = j - L::STEP, sp = (jp + L::NST) % L::NST;
+          if (n > 0 && jp < ntile) {
+            // O += P V of tile n - 1
+            ok = wait_all(bars.p_full(i), (n - 1) & 1, err);
             if (!ok) break;
             tc_fence_after();
             if (leader) {
+              const uint64_t dv = dv0 + sp * ST16;
 #pragma unroll
               for (int ks = 0; ks < TN / 16; ++ks)
-                mma_bf16_ts(tmem + L::TO + 64 * i, tmem + L::TP + 64 * i + 8 * ks, dv + ks * 128, IDESC_PV,
-                            (j > 1 || ks > 0) ? 1u : 0u);
+                mma_bf16_ts(tmem + L::TO + 64 * i, tmem + L::TP + TN / 2 * i + 8 * ks, dv + ks * 128, L::IDESC_PV,
+                            (n > 1 || ks > 0) ? 1u : 0u);
               mma_commit(bars.pv_done(i));
+              if (L::R == 1 || i == nstream - 1) mma_commit(bars.empty(sp));
             }
             __syncwarp();
           }
         }
-        if (ok && j > 0 && leader) mma_commit(bars.empty((j - 1) % L::NST));
-        __syncwarp();
       }
       if (leader) mma_commit(bars.fin());
       __syncwarp();
       mbar_wait(bars.fin(), 0, err);
     }
-  } else if (warp < 4 * nq) {
+  } else if (warp < L::TWARP * nstream) {
     // ------------------------------------------------------------ softmax
-    constexpr bool QUAD = KIND == QUARTERS;
-    constexpr int NC = QUAD ? 1 : 4;               // 32-key chunks of a tile that a thread takes
-    const int qi = warp >> 2;
-    const int c0 = QUAD ? 32 * (warp & 3) : 0;     // first of its keys
-    const int row = blk.row0 + (QUAD ? lane : qi * TM + (threadIdx.x & 127));
+    constexpr bool QUAD = L::QUAD;
+    constexpr int NC = QUAD ? 1 : 2;               // 32-key chunks of a tile that a thread takes
+    const int i = warp / L::TWARP;                 // stream
+    const int half = QUAD ? 0 : (warp >> 2) & 1;
+    const int first = L::R > 1 ? 0 : i;
+    const int count = first < ntile ? (ntile - first + L::STEP - 1) / L::STEP : 0;
+    const int c0 = QUAD ? 32 * warp : 64 * half;   // first of its keys
+    const int r = threadIdx.x & 127;               // row in the tile = TMEM lane
+    const int pair_bar = 2 + (warp & 3) + 4 * i;   // both warps of these 32 rows
+    float* xch = reinterpret_cast<float*>(smem + L::XCH) + i * TM + r;
+    const int row = blk.row0 + (QUAD ? lane : (L::R > 1 ? i * TM : 0) + r);
     const bool real = row < blk.rows;
     const int token = real ? row / a.group : 0;
     const int head = blk.h * a.group + (real ? row - token * a.group : 0);
+    const int at = blk.seq.first + token;
     const int lim = real ? row_limit(a, blk, token) : 0x7fffffff;    // rows without a query need no mask
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t tS = tmem + lane_off + 128 * qi + c0;
-    const uint32_t tO = tmem + lane_off + L::TO + 64 * qi;
-    const uint32_t tP = tmem + lane_off + L::TP + 64 * qi;
+    const uint32_t tS = tmem + lane_off + TN * i + c0;
+    const uint32_t tO = tmem + lane_off + L::TO + 64 * i;
+    const uint32_t tP = tmem + lane_off + L::TP + TN / 2 * i;
     const float sl2 = a.scale_log2;
-    // this row of Q, into the 128-byte swizzle of the operand
-    if (ntile > 0) {
-      uint4 w[8];
+    if (L::R > 1 || i == 0) {
+      // this row of Q, into the 128-byte swizzle of the operand
+      constexpr int CH = 8 / L::HALVES;            // each warp of a pair one half of it
+      uint4 w[CH];
       const uint4* src = reinterpret_cast<const uint4*>(
-          static_cast<const __nv_bfloat16*>(a.q.p) + (blk.seq.first + token) * a.q.st + head * a.q.sh);
+          static_cast<const __nv_bfloat16*>(a.q.p) + at * a.q.st + head * a.q.sh) + CH * half;
 #pragma unroll
-      for (int c = 0; c < 8; ++c) w[c] = real ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
-      const int r = threadIdx.x & 127;
+      for (int c = 0; c < CH; ++c) w[c] = real ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-      for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(smem + qi * TILE + swz(r, c)) = w[c];
+      for (int c = 0; c < CH; ++c)
+        *reinterpret_cast<uint4*>(smem + (L::R > 1 ? i : 0) * QTILE + swz(r, CH * half + c)) = w[c];
       if constexpr (QUAD) {
         // P of the other quarters' keys stays zero
         uint32_t z[32];
@@ -343,181 +482,182 @@ __global__ void __launch_bounds__(Lay<KIND>::NTHREADS, KIND == TWO_TILES ? 1 : 2
     }
     float m = -INFINITY, l = 0.f;
     bool ok = true;
-    for (int j = 0; j < ntile; ++j) {
-      ok = __all_sync(0xffffffffu, mbar_wait(bars.s_full(qi), j & 1, err));
-      if (!ok) break;
-      tc_fence_after();
+    // a wait that ran out skips the later waits, not the steps: the two warps of a pair
+    // meet at the same barriers whatever either of them saw
+    for (int n = 0; n < count; ++n) {
+      const int j = first + n * L::STEP;
       const int kb = (blk.t_begin + j) * TN + c0;
-      const uint32_t bad = info[L::NST];
+      ok = ok && wait_all(bars.s_full(i), n & 1, err);
+      tc_fence_after();
+      const bool bad = info[L::NST] != 0;          // some box had no page
       uint32_t v[32 * NC];
-      if constexpr (QUAD) {
-        tmem_ld32(tS, v);
-      } else {
-        tmem_ld64(tS, v);
-        tmem_ld64(tS + 64, v + 64);
-      }
-      tmem_wait_ld();
-      tc_fence_before();
-      warp_arrive(bars.s_free(qi));
-      if (bad) {
-        // some box of this block had no page: the stage's valid boxes, from its barrier's phase
-        ok = __all_sync(0xffffffffu, mbar_wait(bars.full(j % L::NST), (j / L::NST) & 1, err));
-        if (!ok) break;
-        const uint32_t bits = info[j % L::NST];
 #pragma unroll
-        for (int c = 0; c < NC; ++c) {
-          uint32_t msk = 0;
-          for (int e = 0; e < 32; ++e) msk |= ((bits >> ((c0 + 32 * c + e) >> box_shift)) & 1u) << e;
-          apply_mask(v + 32 * c, msk);
+      for (int c = 0; c < NC; ++c) tmem_ld32(tS + 32 * c, v + 32 * c);
+      tmem_wait_ld();
+      tie<32 * NC>(v);
+      tc_fence_before();
+      warp_arrive(bars.s_free(i));
+      const bool masked = __any_sync(0xffffffffu, kb + 32 * NC > lim || bad);
+      if (masked) {
+        // keys of the tile that this row sees: below its limit, in pages that exist (a stage's
+        // valid boxes are read in its barrier's phase; it is not refilled before this tile's product)
+        uint32_t boxes = ~0u;
+        if (bad) {
+          ok = ok && wait_all(bars.full(j % L::NST), (j / L::NST) & 1, err);
+          boxes = info[j % L::NST];
         }
-      }
-      if (__any_sync(0xffffffffu, kb + 32 * NC > lim)) {
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
           const int left = lim - kb - 32 * c;
-          apply_mask(v + 32 * c, left >= 32 ? ~0u : (left <= 0 ? 0u : (1u << left) - 1u));
+          uint32_t msk = left >= 32 ? ~0u : (left <= 0 ? 0u : (1u << left) - 1u);
+          // 16-key groups: no box is smaller
+          if (!((boxes >> ((c0 + 32 * c) >> box_shift)) & 1u)) msk &= 0xffff0000u;
+          if (!((boxes >> ((c0 + 32 * c + 16) >> box_shift)) & 1u)) msk &= 0x0000ffffu;
+          apply_mask(v + 32 * c, msk);
         }
       }
-      float mx = max32(v);
-#pragma unroll
-      for (int c = 1; c < NC; ++c) mx = fmaxf(mx, max32(v + 32 * c));
+      float mx = row_max<32 * NC>(v);
       // move the reference max only when a row's max grew by more than 2^8
-      const float m_new = fmaxf(m, mx);
-      const bool need = (m == -INFINITY) ? (m_new != -INFINITY) : ((m_new - m) * sl2 > RESCALE_LOG2);
+      bool grow = (m == -INFINITY) ? (mx != -INFINITY) : ((mx - m) * sl2 > RESCALE_LOG2);
+      grow = QUAD ? __any_sync(0xffffffffu, grow) : pair_any(pair_bar, grow);
       float alpha = 1.f;
-      if (need) {
-        alpha = (m == -INFINITY) ? 0.f : ex2((m - m_new) * sl2);
-        m = m_new;
+      if (grow) {
+        if constexpr (!QUAD) {
+          // the maximum of both halves: a row's weights share one reference
+          if (half == 0) *xch = mx;
+          named_bar(pair_bar, 64);
+          if (half == 1) *xch = mx = fmaxf(mx, *xch);
+          named_bar(pair_bar, 64);
+          if (half == 0) mx = *xch;
+        }
+        const float m_new = fmaxf(m, mx);
+        const bool need = (m == -INFINITY) ? (m_new != -INFINITY) : ((m_new - m) * sl2 > RESCALE_LOG2);
+        if (need) {
+          alpha = (m == -INFINITY) ? 0.f : ex2((m - m_new) * sl2);
+          m = m_new;
+        }
+        l *= alpha;
+        grow = __any_sync(0xffffffffu, need && alpha != 0.f);
       }
-      l *= alpha;
       // P (and O) are free once the previous tile's product has completed
-      if (j > 0) {
-        ok = __all_sync(0xffffffffu, mbar_wait(bars.pv_done(qi), (j - 1) & 1, err));
-        if (!ok) break;
+      if (n > 0) {
+        ok = ok && wait_all(bars.pv_done(i), (n - 1) & 1, err);
         tc_fence_after();
-        if (__any_sync(0xffffffffu, need && alpha != 0.f)) {
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            uint32_t w[32];
-            tmem_ld32(tO + 32 * c, w);
+        if (grow) {
+          // each warp of a pair scales its half of the channels
+#pragma unroll 1
+          for (int c = 0; c < 8 / L::HALVES; ++c) {
+            uint32_t w[8];
+            tmem_ld8(tO + 32 * half + 8 * c, w);
             tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * alpha);
-            tmem_st32(tO + 32 * c, w);
+            for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * alpha);
+            tmem_st8(tO + 32 * half + 8 * c, w);
           }
         }
       }
       const float mb = (m == -INFINITY) ? 0.f : m * sl2;
       float l0 = 0.f, l1 = 0.f;
+      auto weights = [&](auto mixed) {
 #pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        uint32_t pk[16];
+        for (int c = 0; c < NC; ++c) {
+          uint32_t pk[16];
 #pragma unroll
-        for (int e = 0; e < 32; e += 2) {
-          float p0, p1;
-          exp2_pair(v[32 * c + e], v[32 * c + e + 1], sl2, -mb, l0, l1, p0, p1);
-          pk[e >> 1] = pack_bf16(p0, p1);
+          for (int e = 0; e < 32; e += 2) {
+            float p0, p1;
+            if (decltype(mixed)::value && ((e / 2) * FMA_PAIRS) % 16 < FMA_PAIRS)
+              exp2_pair_fma(v[32 * c + e], v[32 * c + e + 1], sl2, -mb, l0, l1, p0, p1);
+            else
+              exp2_pair(v[32 * c + e], v[32 * c + e + 1], sl2, -mb, l0, l1, p0, p1);
+            pk[e >> 1] = pack_bf16(p0, p1);
+          }
+          tmem_st16(tP + (c0 >> 1) + 16 * c, pk);
         }
-        tmem_st16(tP + (c0 >> 1) + 16 * c, pk);
-      }
+      };
+      if (QUAD || masked) weights(std::false_type{});
+      else weights(std::true_type{});
       l += l0 + l1;
       tmem_wait_st();
       tc_fence_before();
-      warp_arrive(bars.p_full(qi));
+      warp_arrive(bars.p_full(i));
     }
-    if (ok && ntile > 0) ok = mbar_wait(bars.pv_done(qi), (ntile - 1) & 1, err);
+    if (ok && count > 0) ok = mbar_wait(bars.pv_done(i), (count - 1) & 1, err);
     ok = __all_sync(0xffffffffu, ok);
     tc_fence_after();
-    float o[64];
-    if (ok && ntile > 0) {
+    constexpr int NE = 64 / L::HALVES;             // channels that a thread holds at the end
+    float o[NE];
+    if (ok && count > 0) {
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        uint32_t v[32];
-        tmem_ld32(tO + 32 * c, v);
+      for (int c = 0; c < NE / 32; ++c) {
+        uint32_t w[32];
+        tmem_ld32(tO + 32 * (half + c), w);
         tmem_wait_ld();
 #pragma unroll
-        for (int e = 0; e < 32; ++e) o[32 * c + e] = __uint_as_float(v[e]);
+        for (int e = 0; e < 32; ++e) o[32 * c + e] = __uint_as_float(w[e]);
       }
     } else {
 #pragma unroll
-      for (int e = 0; e < 64; ++e) o[e] = 0.f;
+      for (int e = 0; e < NE; ++e) o[e] = 0.f;
     }
-    const int at = blk.seq.first + token;
-    const long long prow = (static_cast<long long>(blk.split) * a.n_tokens + at) * a.q.heads + head;
-    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out.p) + at * a.out.st + head * a.out.sh;
-    if constexpr (QUAD) {
-      // join the four quarters: the ring is idle, every copy has been consumed
-      constexpr int PITCH = 66;
+    if constexpr (!QUAD) {
+      // the sum of both halves
+      if (half == 0) *xch = l;
+      named_bar(pair_bar, 64);
+      if (half == 1) *xch = l = l + *xch;
+      named_bar(pair_bar, 64);
+      if (half == 0) l = *xch;
+    }
+    if constexpr (L::R > 1) {
+      if (real) write_row(a, blk, at, head, 32 * half, o, m, l);
+    } else {
+      // Join the streams (or the quarters) of each row.  The ring is idle once all of them are here:
+      // every copy has been consumed by a product that has completed.
       float* part = reinterpret_cast<float*>(smem + L::KV);
-      float* mineq = part + threadIdx.x * PITCH;
-      if (real) {
+      constexpr int PARTS = QUAD ? 4 : L::NS;      // parts of a row
+      constexpr int PROWS = QUAD ? 32 : TM;        // rows
+      named_bar(1, 32 * L::NWARP);
+      if (real && (QUAD || i > 0)) {
+        float* mine = part + (QUAD ? threadIdx.x : r) * PITCH;
 #pragma unroll
-        for (int e = 0; e < 64; ++e) mineq[e] = o[e];
-        mineq[64] = m;
-        mineq[65] = l;
-      }
-      named_bar(1, 128);
-      // four threads per row, sixteen channels each
-      const int r = threadIdx.x >> 2, e0 = (threadIdx.x & 3) * 16;
-      const int row_r = blk.row0 + r;
-      if (row_r < blk.rows) {
-        float mx = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < 4; ++w) mx = fmaxf(mx, part[(32 * w + r) * PITCH + 64]);
-        const float mu = (mx == -INFINITY) ? 0.f : mx;
-        float ls = 0.f, os[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) os[e] = 0.f;
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          const float* p = part + (32 * w + r) * PITCH;
-          const float f = ex2((p[64] - mu) * sl2);
-          ls = fmaf(f, p[65], ls);
-#pragma unroll
-          for (int e = 0; e < 16; ++e) os[e] = fmaf(f, p[e0 + e], os[e]);
+        for (int e = 0; e < NE; ++e) mine[32 * half + e] = o[e];
+        if (half == 0) {
+          mine[64] = m;
+          mine[65] = l;
         }
-        const int tk = row_r / a.group;
-        const int hd = blk.h * a.group + row_r - tk * a.group;
-        const int tat = blk.seq.first + tk;
-        if (a.n_split == 1) {
-          const float inv = ls > 0.f ? 1.f / ls : (ls == ls ? 0.f : ls);
-          __nv_bfloat16* d = static_cast<__nv_bfloat16*>(a.out.p) + tat * a.out.st + hd * a.out.sh + e0;
+      }
+      named_bar(1, 32 * L::NWARP);
+      if constexpr (QUAD) {
+        // four threads per row, sixteen channels each
+        const int rr = threadIdx.x >> 2, e0 = (threadIdx.x & 3) * 16;
+        const int row_r = blk.row0 + rr;
+        if (row_r < blk.rows) {
+          float mx = -INFINITY;
 #pragma unroll
-          for (int e = 0; e < 16; e += 8)
-            *reinterpret_cast<uint4*>(d + e) =
-                make_uint4(pack_bf16(os[e] * inv, os[e + 1] * inv), pack_bf16(os[e + 2] * inv, os[e + 3] * inv),
-                           pack_bf16(os[e + 4] * inv, os[e + 5] * inv), pack_bf16(os[e + 6] * inv, os[e + 7] * inv));
-          if (a.lse && e0 == 0)
-            a.lse[static_cast<long long>(hd) * a.n_tokens + tat] =
-                ls == 0.f ? -INFINITY : (mu * sl2 + log2f(ls)) * LN2;
-        } else {
-          const long long pr = (static_cast<long long>(blk.split) * a.n_tokens + tat) * a.q.heads + hd;
-          if (ntile > 0) {
+          for (int w = 0; w < PARTS; ++w) mx = fmaxf(mx, part[(PROWS * w + rr) * PITCH + 64]);
+          const float mu = (mx == -INFINITY) ? 0.f : mx;
+          float ls = 0.f, os[16];
 #pragma unroll
-            for (int e = 0; e < 16; e += 4)
-              *reinterpret_cast<float4*>(a.part_o + pr * D + e0 + e) =
-                  make_float4(os[e], os[e + 1], os[e + 2], os[e + 3]);
+          for (int e = 0; e < 16; ++e) os[e] = 0.f;
+#pragma unroll
+          for (int w = 0; w < PARTS; ++w) {
+            const float* p = part + (PROWS * w + rr) * PITCH;
+            const float f = ex2((p[64] - mu) * sl2);
+            ls = fmaf(f, p[65], ls);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) os[e] = fmaf(f, p[e0 + e], os[e]);
           }
-          if (e0 == 0) *reinterpret_cast<float2*>(a.part_ml + pr * 2) = make_float2(mx, ls);
+          const int tk = row_r / a.group;
+          write_row(a, blk, blk.seq.first + tk, blk.h * a.group + row_r - tk * a.group, e0, os, mx, ls);
         }
-      }
-    } else if (real) {
-      if (a.n_split == 1) {
-        const float inv = l > 0.f ? 1.f / l : (l == l ? 0.f : l);     // a NaN stays one
+      } else if (i == 0 && real) {
+        const float* p = part + r * PITCH;
+        const float mx = fmaxf(m, p[64]);
+        const float mu = (mx == -INFINITY) ? 0.f : mx;
+        const float f0 = ex2((m - mu) * sl2), f1 = ex2((p[64] - mu) * sl2);
+        l = fmaf(f1, p[65], f0 * l);
 #pragma unroll
-        for (int e = 0; e < 64; e += 8)
-          *reinterpret_cast<uint4*>(dst + e) =
-              make_uint4(pack_bf16(o[e] * inv, o[e + 1] * inv), pack_bf16(o[e + 2] * inv, o[e + 3] * inv),
-                         pack_bf16(o[e + 4] * inv, o[e + 5] * inv), pack_bf16(o[e + 6] * inv, o[e + 7] * inv));
-        if (a.lse)
-          a.lse[static_cast<long long>(head) * a.n_tokens + at] = l == 0.f ? -INFINITY : (m * sl2 + log2f(l)) * LN2;
-      } else {
-        if (ntile > 0) {
-#pragma unroll
-          for (int e = 0; e < 64; e += 4)
-            *reinterpret_cast<float4*>(a.part_o + prow * D + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-        }
-        *reinterpret_cast<float2*>(a.part_ml + prow * 2) = make_float2(m, l);
+        for (int e = 0; e < NE; ++e) o[e] = fmaf(f1, p[32 * half + e], f0 * o[e]);
+        write_row(a, blk, at, head, 32 * half, o, mx, l);
       }
     }
   }
@@ -751,14 +891,14 @@ __global__ void __launch_bounds__(128) cache_join_kernel(const __grid_constant__
 }
 
 // ---- host -------------------------------------------------------------------------
-// a pool of pages as [rows][64] with boxes of one page (at most 128 rows)
-bool pool_map(CUtensorMap* m, const void* base, const PagedCache& c) {
+// a pool of pages as [rows][64] with boxes of one page (at most a tile's keys)
+bool pool_map(CUtensorMap* m, const void* base, const PagedCache& c, int keys) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
   const int page = 1 << c.page_shift;
   const cuuint64_t dims[2] = {64, static_cast<cuuint64_t>(c.num_pages) * c.heads * page};
   const cuuint64_t strides[1] = {128};
-  const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(page < TN ? page : TN)};
+  const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(page < keys ? page : keys)};
   const cuuint32_t estr[2] = {1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -784,7 +924,7 @@ cudaError_t launch_tc(const CacheAttnArgs& a, unsigned blocks, cudaStream_t st) 
   cudaError_t e = allow_smem(cache_attn_kernel<KIND>, L::BYTES, done);
   if (e != cudaSuccess) return e;
   CUtensorMap mk, mv;
-  if (!pool_map(&mk, a.c.k, a.c) || !pool_map(&mv, a.c.v, a.c)) return cudaErrorInvalidValue;
+  if (!pool_map(&mk, a.c.k, a.c, L::TK) || !pool_map(&mv, a.c.v, a.c, L::TK)) return cudaErrorInvalidValue;
   cache_attn_kernel<KIND><<<blocks, L::NTHREADS, L::BYTES, st>>>(mk, mv, a);
   return cudaGetLastError();
 }
@@ -805,47 +945,58 @@ CacheAttnPlan plan_cache_attn(bool fp32, int batch, int kv_heads, int q_heads, l
   CacheAttnPlan p;
   const long long most = n_tokens < max_new ? n_tokens : max_new;
   const long long rows = most * (q_heads / kv_heads);
-  int tile, keys, slots, least;      // rows and keys per tile, blocks that run at once, key tiles worth a split
+  // rows and keys per tile, rows that a block counts in, blocks that run at once, key tiles
+  // worth a split, key tiles that a block's start costs
+  int tile, keys, unit, slots, least;
+  double start;
   if (fp32) {
     p.kind = rows <= 16 ? F32_16 : F32_64;
-    tile = rows <= 16 ? 16 : 64;
+    tile = unit = rows <= 16 ? 16 : 64;
     keys = FK;
     slots = 296;
-    least = 4;
+    least = 2;
+    start = 0.3;
   } else if (rows <= 32) {
     p.kind = QUARTERS;
-    tile = 32;
-    keys = TN;
+    tile = unit = 32;
+    keys = Lay<QUARTERS>::TK;
     slots = 296;
     least = 4;
+    start = 1;
   } else if (rows <= 128) {
     p.kind = ONE_TILE;
-    tile = 128;
-    keys = TN;
-    slots = 296;
+    tile = unit = 128;
+    keys = Lay<ONE_TILE>::TK;
+    slots = 148;
     least = 4;
+    start = 2;
   } else {
-    p.kind = TWO_TILES;
-    tile = 256;
-    keys = TN;
+    p.kind = ROW_TILES;
+    tile = Lay<ROW_TILES>::ROWS;
+    unit = 128;
+    keys = Lay<ROW_TILES>::TK;
     slots = 148;
     least = 16;
+    start = 3;
   }
   p.row_tiles = static_cast<int>((rows + tile - 1) / tile);
   if (p.row_tiles < 1) p.row_tiles = 1;
-  const long long blocks = static_cast<long long>(batch) * kv_heads * p.row_tiles;
+  const long long heads = static_cast<long long>(batch) * kv_heads;
   const long long ktiles = (max_len + keys - 1) / keys;
   long long ns = 1, most_splits = ktiles / least;
   if (most_splits > 128) most_splits = 128;
-  if (blocks < 2 * slots && most_splits > 1) {
-    // the fewest splits that fill the last wave best
-    double best = 0.0;
-    const long long top = (4 * slots + blocks - 1) / blocks;
-    for (long long n = 1; n <= most_splits && n <= top; ++n) {
-      const long long tot = blocks * n;
-      const double eff = static_cast<double>(tot) / static_cast<double>(slots * ((tot + slots - 1) / slots));
-      if (eff > best + 0.02) {
-        best = eff;
+  if (most_splits > 1) {
+    // Rounds that the blocks take on the GPU in units of one unsplit block (a block with one of
+    // its two row tiles counts less), with the cost of a block's start and of joining its part
+    // as some key tiles more.
+    const long long units = (rows + unit - 1) / unit;
+    // a block with one of its two row tiles takes four fifths of the time
+    const double load = heads * (units / (tile / unit) + (units % (tile / unit) ? 0.8 : 0.0)) / slots;
+    double best = 1e30;
+    for (long long n = 1; n <= most_splits && (n == 1 || load < 2.0) && (n - 1) * load < 4.0; ++n) {
+      const double t = ceil(load * n) / n + start * n / ktiles;
+      if (t < best * 0.99) {
+        best = t;
         ns = n;
       }
     }
@@ -860,7 +1011,7 @@ cudaError_t launch_cache_attn(const CacheAttnArgs& a, bool fp32, int kind, cudaS
   const unsigned blocks = static_cast<unsigned>(a.c.batch) * a.c.heads * a.row_tiles * a.n_split;
   cudaError_t e;
   switch (kind) {
-    case TWO_TILES: e = launch_tc<TWO_TILES>(a, blocks, st); break;
+    case ROW_TILES: e = launch_tc<ROW_TILES>(a, blocks, st); break;
     case ONE_TILE: e = launch_tc<ONE_TILE>(a, blocks, st); break;
     case QUARTERS: e = launch_tc<QUARTERS>(a, blocks, st); break;
     case F32_64: e = launch_f32<64>(a, blocks, st); break;
