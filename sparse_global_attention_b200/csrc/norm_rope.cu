@@ -1,17 +1,23 @@
 // Per-head norm of queries and keys with the position rotation in one pass,
 // its gradients, and the same pass writing keys (and values) into a paged cache.
 //
-// A row is the 64 channels of one (token, head).  Eight lanes hold a row, eight
-// channels each, so a warp works on four heads of a token at a time with one
-// 16-byte (bf16) access per lane, and every sum over a row is three shuffles.
-// Mean and variance come from the row in registers (the variance from the
-// centred values), the rotation pairs are a lane exchange (channel i with i + 32:
-// lane ^ 4; i with i + 16 inside a half: lane ^ 2), everything in fp32 with one
-// rounding at the store.  One warp takes one token: its 32 angles are computed
-// once, one per lane, and serve all heads.  An angle is reduced to a part of a
-// turn in 64 bits (position times turns per position, minus the nearest whole
-// number), so positions far into a stream lose nothing; what is left goes to
-// sincospif.
+// A row is the 64 channels of one (token, head).  Eight lanes hold a row, so a warp
+// works on four heads of a token at a time (a quad) and every sum over a row is three
+// shuffles.  A lane holds four channels and the four that the rotation pairs them with
+// (i and i + 32, or i and i + 16 inside a half), so the rotation needs no exchange, and
+// the arithmetic runs on pairs of channels (packed fp32: the passes are near the issue
+// limit, 1,800 instructions a token of 16 heads in the one-channel form with exchanged
+// partners took 123 us where the bytes take 78).  Mean and variance come from the row in
+// registers (the variance from the centred values), everything is fp32 with one rounding
+// at the store.  The 32 angles of a token are computed once, one per lane, and serve all
+// its heads.  An angle is a part of a turn in 64-bit fixed point (position times turns per
+// position modulo 2^64 is one integer product, off by 2^-34 of a turn at the most), so
+// positions far into a stream lose nothing; its upper half goes to sincospif.
+//
+// Bound by HBM.  Each warp loads all quads of its item before it works on them; a grid of
+// what the SMs hold keeps the tokens in flight together, so that the rows of each head are
+// written side by side (128 frames of 1296 tokens and 16 heads, 2.04 GB: 393 us, 5.2 TB/s;
+// a block for every eight tokens instead: 503 us).
 #include "gsa_common.cuh"
 #include "operators.h"
 
@@ -21,43 +27,85 @@ namespace {
 
 constexpr int NTHR = 256;
 constexpr int WARPS = NTHR / 32;
+constexpr int FWD_BLOCKS = 148 * 3;      // of the forward at the most: what the SMs hold
 
-// eight consecutive channels, kept as loaded until they are used
-template <typename T> struct Raw8;
-template <> struct Raw8<__nv_bfloat16> {
-  uint4 u;
-  __device__ __forceinline__ void load(const void* p) { u = __ldcs(reinterpret_cast<const uint4*>(p)); }
-  __device__ __forceinline__ void zero() { u = make_uint4(0, 0, 0, 0); }
-  __device__ __forceinline__ void get(float* f) const {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f[2 * i] = __uint_as_float(w[i] << 16);
-      f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-  }
-  __device__ __forceinline__ void put(const float* f) {
-    u = make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
-  }
-  __device__ __forceinline__ void store(void* p) const { *reinterpret_cast<uint4*>(p) = u; }
+// ---- pairs of channels ----------------------------------------------------------
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n .reg .b64 a, b;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n add.rn.f32x2 a, a, b;\n"
+      " mov.b64 {%0, %1}, a;\n}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n .reg .b64 a, b;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mul.rn.f32x2 a, a, b;\n"
+      " mov.b64 {%0, %1}, a;\n}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n .reg .b64 a, b, c;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mov.b64 c, {%6, %7};\n"
+      " fma.rn.f32x2 a, a, b, c;\n mov.b64 {%0, %1}, a;\n}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+// a lane's eight channels: 0..3 and, in 4..7, the ones that the rotation pairs with them
+struct Lane8 {
+  float2 v[4];
 };
-template <> struct Raw8<float> {
-  float4 a, b;
-  __device__ __forceinline__ void load(const void* p) {
-    a = __ldcs(reinterpret_cast<const float4*>(p));
-    b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+
+// four channels, kept as loaded until they are used
+template <typename T> struct Raw4;
+template <> struct Raw4<__nv_bfloat16> {
+  uint2 u;
+  __device__ __forceinline__ void load(const void* p) { u = __ldcg(static_cast<const uint2*>(p)); }
+  __device__ __forceinline__ void zero() { u = make_uint2(0, 0); }
+  __device__ __forceinline__ void get(float2* f) const {
+    f[0] = make_float2(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u));
+    f[1] = make_float2(__uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
   }
-  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
-  __device__ __forceinline__ void get(float* f) const {
-    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w; f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+  __device__ __forceinline__ void put(const float2* f) {
+    u = make_uint2(pack_bf16(f[0].x, f[0].y), pack_bf16(f[1].x, f[1].y));
   }
-  __device__ __forceinline__ void put(const float* f) {
-    a = make_float4(f[0], f[1], f[2], f[3]);
-    b = make_float4(f[4], f[5], f[6], f[7]);
+  __device__ __forceinline__ void store(void* p) const { __stcs(static_cast<uint2*>(p), u); }
+};
+template <> struct Raw4<float> {
+  float4 u;
+  __device__ __forceinline__ void load(const void* p) { u = __ldcg(static_cast<const float4*>(p)); }
+  __device__ __forceinline__ void zero() { u = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void get(float2* f) const {
+    f[0] = make_float2(u.x, u.y);
+    f[1] = make_float2(u.z, u.w);
   }
-  __device__ __forceinline__ void store(void* p) const {
-    reinterpret_cast<float4*>(p)[0] = a;
-    reinterpret_cast<float4*>(p)[1] = b;
+  __device__ __forceinline__ void put(const float2* f) { u = make_float4(f[0].x, f[0].y, f[1].x, f[1].y); }
+  __device__ __forceinline__ void store(void* p) const { __stcs(static_cast<float4*>(p), u); }
+};
+template <typename T>
+struct Raw8 {
+  Raw4<T> a, b;
+  __device__ __forceinline__ void get(Lane8& x) const {
+    a.get(x.v);
+    b.get(x.v + 2);
+  }
+  __device__ __forceinline__ void put(const Lane8& x) {
+    a.put(x.v);
+    b.put(x.v + 2);
+  }
+};
+
+// first channel of a lane, and the distance to its partners
+template <int AXES>
+struct Chan {
+  static constexpr int APART = AXES == 0 ? 4 : (AXES == 1 ? 32 : 16);
+  __device__ static __forceinline__ int first(int c) {
+    return AXES == 0 ? 8 * c : (AXES == 1 ? 4 * c : 32 * (c >> 2) + 4 * (c & 3));
   }
 };
 
@@ -67,95 +115,103 @@ __device__ __forceinline__ float row_sum(float v) {      // over the eight lanes
   v += __shfl_xor_sync(0xffffffffu, v, 4);
   return v;
 }
+__device__ __forceinline__ float sum8(float2 a, float2 b, float2 c, float2 d) {
+  const float2 s = add2(add2(a, b), add2(c, d));
+  return row_sum(s.x + s.y);
+}
 
-// cos and sin of this lane's eight channels for a token at positions p0, p1
+// cos and sin of this lane's four pairs for a token at positions p0, p1
 template <int AXES>
 struct Turn {
-  float c[8], s[8];          // s carries the sign of the channel's place in its pair
-  __device__ __forceinline__ void set(double f, long long p0, long long p1, int lane) {
-    const long long p = (AXES == 2 && lane >= 16) ? p1 : p0;
-    double t = static_cast<double>(p) * f;
-    t -= rint(t);
+  float2 c[2], s[2], ns[2];
+  __device__ __forceinline__ void set(unsigned long long f, int p0, int p1, int lane) {
+    const long long p = AXES == 2 && lane >= 16 ? p1 : p0;
+    const long long turn = static_cast<long long>(static_cast<unsigned long long>(p) * f);      // modulo a turn
     float sn, cs;
-    sincospif(static_cast<float>(2.0 * t), &sn, &cs);
-    const int ch = lane & 7;
-    const int from = AXES == 2 ? 16 * (ch >> 2) + 8 * (ch & 1) : 8 * (ch & 3);
-    const bool first = AXES == 2 ? (ch & 2) == 0 : ch < 4;
+    sincospif(static_cast<float>(static_cast<int>(turn >> 32)) * 4.656612873077393e-10f, &sn, &cs);   // 2^-31 half turns
+    const int from = 4 * (lane & 7);
+    float* cp = reinterpret_cast<float*>(c);
+    float* sp = reinterpret_cast<float*>(s);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      c[e] = __shfl_sync(0xffffffffu, cs, from + e);
-      const float v = __shfl_sync(0xffffffffu, sn, from + e);
-      s[e] = first ? -v : v;
+    for (int e = 0; e < 4; ++e) {
+      cp[e] = __shfl_sync(0xffffffffu, cs, from + e);
+      sp[e] = __shfl_sync(0xffffffffu, sn, from + e);
     }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) ns[k] = make_float2(-s[k].x, -s[k].y);
   }
   // rotate by the angle (DIR = 1) or back (DIR = -1)
   template <int DIR>
-  __device__ __forceinline__ void apply(float* y) const {
+  __device__ __forceinline__ void apply(Lane8& y) const {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float o = __shfl_xor_sync(0xffffffffu, y[e], AXES == 2 ? 2 : 4);
-      y[e] = DIR > 0 ? fmaf(o, s[e], y[e] * c[e]) : fmaf(-o, s[e], y[e] * c[e]);
+    for (int k = 0; k < 2; ++k) {
+      const float2 a = y.v[k], b = y.v[2 + k];
+      y.v[k] = fma2(b, DIR > 0 ? ns[k] : s[k], mul2(a, c[k]));
+      y.v[2 + k] = fma2(a, DIR > 0 ? s[k] : ns[k], mul2(b, c[k]));
     }
   }
 };
 template <>
 struct Turn<0> {
-  __device__ __forceinline__ void set(double, long long, long long, int) {}
+  __device__ __forceinline__ void set(unsigned long long, int, int, int) {}
   template <int DIR>
-  __device__ __forceinline__ void apply(float*) const {}
+  __device__ __forceinline__ void apply(Lane8&) const {}
 };
 
-// turns per unit of position of this lane's channel pair
+// turns per unit of position of this lane's channel pair, in 2^-64
 template <int AXES>
-__device__ __forceinline__ double lane_freq(const RopeTable& r, int lane) {
-  if constexpr (AXES == 0) return 0.0;
+__device__ __forceinline__ unsigned long long lane_freq(const RopeTable& r, int lane) {
+  if constexpr (AXES == 0) return 0;
   return r.f[AXES == 2 ? (lane & 15) : lane];
 }
 
 // normalised row (no weight); returns the row's factor
 template <int NORM>
-__device__ __forceinline__ float norm_row(float* x, float eps) {
+__device__ __forceinline__ float norm_row(Lane8& x, float eps) {
   if constexpr (NORM == NORM_NONE) return 1.f;
   if constexpr (NORM == NORM_LAYER) {
-    float s = 0.f;
+    const float2 nm = both(sum8(x.v[0], x.v[1], x.v[2], x.v[3]) * (-1.f / D));
 #pragma unroll
-    for (int e = 0; e < 8; ++e) s += x[e];
-    const float mean = row_sum(s) * (1.f / D);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] -= mean;
+    for (int k = 0; k < 4; ++k) x.v[k] = add2(x.v[k], nm);
   }
-  float q = 0.f;
+  float2 q = mul2(x.v[0], x.v[0]);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) q = fmaf(x[e], x[e], q);
-  const float r = 1.f / sqrtf(row_sum(q) * (1.f / D) + eps);
+  for (int k = 1; k < 4; ++k) q = fma2(x.v[k], x.v[k], q);
+  const float r = rsqrtf(fmaf(row_sum(q.x + q.y), 1.f / D, eps));
+  const float2 rr = both(r);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) x[e] *= r;
+  for (int k = 0; k < 4; ++k) x.v[k] = mul2(x.v[k], rr);
   return r;
 }
 
 // weight and bias of a lane's eight channels
 template <typename T, int NORM>
 struct Affine {
-  float w[8], b[8];
-  __device__ __forceinline__ void load(const void* wp, const void* bp, int ch) {
+  Lane8 w, b;
+  __device__ __forceinline__ void load(const void* wp, const void* bp, int first, int apart) {
     Raw8<T> r;
-    r.load(static_cast<const T*>(wp) + 8 * ch);
+    r.a.load(static_cast<const T*>(wp) + first);
+    r.b.load(static_cast<const T*>(wp) + first + apart);
     r.get(w);
     if constexpr (NORM == NORM_LAYER) {
-      r.zero();
-      if (bp) r.load(static_cast<const T*>(bp) + 8 * ch);
+      r.a.zero();
+      r.b.zero();
+      if (bp) {
+        r.a.load(static_cast<const T*>(bp) + first);
+        r.b.load(static_cast<const T*>(bp) + first + apart);
+      }
       r.get(b);
     }
   }
-  __device__ __forceinline__ void apply(float* x) const {
+  __device__ __forceinline__ void apply(Lane8& x) const {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = NORM == NORM_LAYER ? fmaf(x[e], w[e], b[e]) : x[e] * w[e];
+    for (int k = 0; k < 4; ++k) x.v[k] = NORM == NORM_LAYER ? fma2(x.v[k], w.v[k], b.v[k]) : mul2(x.v[k], w.v[k]);
   }
 };
 template <typename T>
 struct Affine<T, NORM_NONE> {
-  __device__ __forceinline__ void load(const void*, const void*, int) {}
-  __device__ __forceinline__ void apply(float*) const {}
+  __device__ __forceinline__ void load(const void*, const void*, int, int) {}
+  __device__ __forceinline__ void apply(Lane8&) const {}
 };
 
 __device__ __forceinline__ void split_token(long long g, long long n_tokens, long long& o, long long& t) {
@@ -166,194 +222,6 @@ __device__ __forceinline__ void split_token(long long g, long long n_tokens, lon
   } else {
     o = g / n_tokens;
     t = g - o * n_tokens;
-  }
-}
-
-// the heads of one token, 4 U at a time: load, fn(row in registers), store
-template <typename TI, typename TO, int U, typename F>
-__device__ __forceinline__ void each_row(const TI* in, long long in_sh, TO* out, long long out_sh, int heads, int lane,
-                                         F fn) {
-  const int r = lane >> 3, ch = lane & 7;
-#pragma unroll 1
-  for (int h0 = 0; h0 < heads; h0 += 4 * U) {
-    Raw8<TI> raw[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int h = h0 + 4 * u + r;
-      if (h < heads) raw[u].load(in + h * in_sh + 8 * ch);
-      else raw[u].zero();
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int h = h0 + 4 * u + r;
-      if (h0 + 4 * u >= heads) break;      // the whole warp
-      float x[8];
-      raw[u].get(x);
-      fn(x);
-      Raw8<TO> w;
-      w.put(x);
-      if (h < heads) w.store(out + h * out_sh + 8 * ch);
-    }
-  }
-}
-
-// blockIdx.y: 0 queries, 1 keys, 2 values (carried along)
-template <typename T, int NORM, int AXES>
-__global__ void __launch_bounds__(NTHR) norm_rope_kernel(const __grid_constant__ NormRopeArgs a) {
-  constexpr int U = sizeof(T) == 2 ? 4 : 2;
-  const int role = blockIdx.y;
-  const Rows in = a.in[role], out = a.out[role];
-  if (in.heads == 0) return;
-  const int lane = threadIdx.x & 31;
-  const T* src = static_cast<const T*>(in.p);
-  T* dst = static_cast<T*>(out.p);
-  const long long total = a.n_outer * a.n_tokens, step = static_cast<long long>(gridDim.x) * WARPS;
-  Affine<T, NORM> af;
-  if (role < 2) af.load(a.w[role], a.b[role], lane & 7);
-  const double f = lane_freq<AXES>(a.rope, lane);
-  for (long long g = static_cast<long long>(blockIdx.x) * WARPS + (threadIdx.x >> 5); g < total; g += step) {
-    long long o, t;
-    split_token(g, a.n_tokens, o, t);
-    const T* pi = src + o * in.so + t * in.st;
-    T* po = dst + o * out.so + t * out.st;
-    if (role == 2) {
-      each_row<T, T, U>(pi, in.sh, po, out.sh, in.heads, lane, [](float*) {});
-      continue;
-    }
-    Turn<AXES> turn;
-    if constexpr (AXES > 0) {
-      const int* p = a.pos + o * a.pos_so + t * AXES;
-      turn.set(f, p[0], AXES == 2 ? p[AXES - 1] : 0, lane);
-    }
-    each_row<T, T, U>(pi, in.sh, po, out.sh, in.heads, lane, [&](float* x) {
-      norm_row<NORM>(x, a.eps);
-      af.apply(x);
-      turn.template apply<1>(x);
-    });
-  }
-}
-
-// Gradients: with g the output gradient turned back and h the normalised row,
-// db += g, dw += g h, u = g w, dx = r (u - mean(u) - h mean(u h)) (RMS: without
-// mean(u)).  A block's weight sums go to its own row of `part`; a second kernel
-// adds those in a fixed order.
-template <typename T, typename G, int NORM, int AXES>
-__global__ void __launch_bounds__(NTHR) norm_rope_bwd_kernel(const __grid_constant__ NormRopeBwdArgs a) {
-  constexpr int U = 2;
-  const int role = blockIdx.y;
-  const Rows gin = a.dout[role], gout = a.din[role];
-  if (gin.heads == 0) return;
-  const int lane = threadIdx.x & 31, r = lane >> 3, ch = lane & 7;
-  const long long total = a.n_outer * a.n_tokens, step = static_cast<long long>(gridDim.x) * WARPS;
-  const double f = lane_freq<AXES>(a.rope, lane);
-  Affine<T, NORM == NORM_NONE ? NORM_NONE : NORM_RMS> af;
-  const int xr = role < 2 ? role : 0;
-  const Rows xin = a.in[xr];
-  if (role < 2) af.load(a.w[role], nullptr, ch);
-  float dw[8], db[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) dw[e] = db[e] = 0.f;
-  for (long long g = static_cast<long long>(blockIdx.x) * WARPS + (threadIdx.x >> 5); g < total; g += step) {
-    long long o, t;
-    split_token(g, a.n_tokens, o, t);
-    const G* pg = static_cast<const G*>(gin.p) + o * gin.so + t * gin.st;
-    G* po = static_cast<G*>(gout.p) + o * gout.so + t * gout.st;
-    if (role == 2) {
-      each_row<G, G, U>(pg, gin.sh, po, gout.sh, gin.heads, lane, [](float*) {});
-      continue;
-    }
-    const T* px = static_cast<const T*>(xin.p) + o * xin.so + t * xin.st;
-    Turn<AXES> turn;
-    if constexpr (AXES > 0) {
-      const int* p = a.pos + o * a.pos_so + t * AXES;
-      turn.set(f, p[0], AXES == 2 ? p[AXES - 1] : 0, lane);
-    }
-#pragma unroll 1
-    for (int h0 = 0; h0 < gin.heads; h0 += 4 * U) {
-      Raw8<G> rg[U];
-      Raw8<T> rx[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int h = h0 + 4 * u + r;
-        rg[u].zero();
-        rx[u].zero();
-        if (h < gin.heads) {
-          rg[u].load(pg + h * gin.sh + 8 * ch);
-          if constexpr (NORM != NORM_NONE) rx[u].load(px + h * xin.sh + 8 * ch);
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int h = h0 + 4 * u + r;
-        if (h0 + 4 * u >= gin.heads) break;
-        float d[8];
-        rg[u].get(d);
-        turn.template apply<-1>(d);
-        if constexpr (NORM != NORM_NONE) {
-          float x[8];
-          rx[u].get(x);
-          const float rs = norm_row<NORM>(x, a.eps);
-          float su = 0.f, sh = 0.f;
-          const bool real = h < gin.heads;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            if (real) {
-              db[e] += d[e];
-              dw[e] = fmaf(d[e], x[e], dw[e]);
-            }
-            d[e] *= af.w[e];
-            su += d[e];
-            sh = fmaf(d[e], x[e], sh);
-          }
-          const float mh = row_sum(sh) * (1.f / D);
-          const float mu = NORM == NORM_LAYER ? row_sum(su) * (1.f / D) : 0.f;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) d[e] = rs * (d[e] - mu - x[e] * mh);
-        }
-        Raw8<G> w;
-        w.put(d);
-        if (h < gin.heads) w.store(po + h * gout.sh + 8 * ch);
-      }
-    }
-  }
-  if constexpr (NORM != NORM_NONE) {
-    if (role == 2 || !a.part) return;
-    __shared__ float sums[WARPS][128];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      dw[e] += __shfl_xor_sync(0xffffffffu, dw[e], 8);
-      dw[e] += __shfl_xor_sync(0xffffffffu, dw[e], 16);
-      db[e] += __shfl_xor_sync(0xffffffffu, db[e], 8);
-      db[e] += __shfl_xor_sync(0xffffffffu, db[e], 16);
-      if (r == 0) {
-        sums[threadIdx.x >> 5][8 * ch + e] = dw[e];
-        sums[threadIdx.x >> 5][64 + 8 * ch + e] = db[e];
-      }
-    }
-    __syncthreads();
-    if (threadIdx.x < 128) {
-      float v = 0.f;
-#pragma unroll
-      for (int w = 0; w < WARPS; ++w) v += sums[w][threadIdx.x];
-      a.part[(static_cast<long long>(role) * a.n_part + blockIdx.x) * 128 + threadIdx.x] = v;
-    }
-  }
-}
-
-// one block per tensor: column c of [n_part][128], eight interleaved chains
-__global__ void __launch_bounds__(1024) norm_rope_sum_kernel(const float* part, int n_part, float* dw0, float* db0,
-                                                             float* dw1, float* db1) {
-  __shared__ float sums[8][128];
-  const int col = threadIdx.x & 127, grp = threadIdx.x >> 7, role = blockIdx.x;
-  float v = 0.f;
-  for (int i = grp; i < n_part; i += 8) v += part[(static_cast<long long>(role) * n_part + i) * 128 + col];
-  sums[grp][col] = v;
-  __syncthreads();
-  if (grp == 0) {
-#pragma unroll
-    for (int i = 1; i < 8; ++i) v += sums[i][col];
-    float* out = col < 64 ? (role ? dw1 : dw0) : (role ? db1 : db0);
-    if (out) out[col & 63] = v;
   }
 }
 
@@ -373,58 +241,288 @@ __device__ __forceinline__ int find_sequence(const int* cu, int n, long long t, 
   return lo;
 }
 
-// blockIdx.y: 0 keys (normed and rotated), 1 values; one warp per token
-template <typename T, int NORM, int AXES>
-__global__ void __launch_bounds__(NTHR) append_kernel(const __grid_constant__ AppendArgs a) {
+// element of new token t in a pool (head 0), -1 if it has no page; and its place in its sequence
+__device__ __forceinline__ long long paged_row(const NormRopeArgs& a, long long t, int lane, int& place) {
+  const PagedCache& c = a.c;
+  if (a.cu[0] > t) return -1;
+  const int b = find_sequence(a.cu, c.batch, t, lane);
+  if (b >= c.batch) return -1;                             // behind the last sequence
+  const int first = a.cu[b], start = a.start[b];
+  const long long at = static_cast<long long>(start) + (t - first);
+  int page = -1;
+  if (first <= t && a.cu[b + 1] > t && start >= 0 && (at >> c.page_shift) < c.max_pages)
+    page = c.table[b * c.table_stride + (at >> c.page_shift)];
+  if (page < 0 || page >= c.num_pages) {
+    if (lane == 0) set_error(a.err, ERR_BOUNDS);
+    return -1;
+  }
+  place = static_cast<int>(at);
+  return ((static_cast<long long>(page) * c.heads << c.page_shift) + (at & ((1 << c.page_shift) - 1))) * D;
+}
+
+// An item is up to U quads of one token: `left` heads from `head` on.
+struct Item {
+  long long o, t;
+  int head;
+  __device__ __forceinline__ void at(long long it, int batches, int heads_per, long long n_tokens) {
+    long long g = it;
+    int hb = 0;
+    if (batches > 1) {
+      long long b;
+      split_token(it, batches, g, b);
+      hb = static_cast<int>(b);
+    }
+    head = hb * heads_per;
+    split_token(g, n_tokens, o, t);
+  }
+};
+
+// Items of q, then of k, then of v (carried along), over all warps of the grid.  PAGED: rows go to
+// the cache instead of `out` (tokens packed, outer 1).
+template <typename T, int NORM, int AXES, bool PAGED>
+__global__ void __launch_bounds__(NTHR, 3) norm_rope_kernel(const __grid_constant__ NormRopeArgs a) {
   constexpr int U = sizeof(T) == 2 ? 4 : 2;
-  const int role = blockIdx.y;
-  const Rows in = a.in[role];
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, r = lane >> 3;
+  const int c0 = Chan<AXES>::first(lane & 7);
+  constexpr int APART = Chan<AXES>::APART;
+  const long long tokens = a.n_outer * a.n_tokens;
   const long long step = static_cast<long long>(gridDim.x) * WARPS;
-  Affine<T, NORM> af;
-  if (role == 0) af.load(a.w, a.b, lane & 7);
-  const double f = lane_freq<AXES>(a.rope, lane);
-  const int page_size = 1 << a.c.page_shift;
-  for (long long t = static_cast<long long>(blockIdx.x) * WARPS + (threadIdx.x >> 5); t < a.n_tokens; t += step) {
-    if (a.cu[0] > t) continue;
-    const int b = find_sequence(a.cu, a.c.batch, t, lane);
-    if (b >= a.c.batch) continue;                       // behind the last sequence
-    const int first = a.cu[b];
-    const long long place = static_cast<long long>(a.start[b]) + (t - first);
-    int page = -1;
-    if (first <= t && a.cu[b + 1] > t && a.start[b] >= 0 && (place >> a.c.page_shift) < a.c.max_pages)
-      page = a.c.table[b * a.c.table_stride + (place >> a.c.page_shift)];
-    if (page < 0 || page >= a.c.num_pages) {
-      if (lane == 0) set_error(a.err, ERR_BOUNDS);
-      continue;
-    }
-    const long long row = (static_cast<long long>(page) * a.c.heads << a.c.page_shift) + (place & (page_size - 1));
-    const T* pi = static_cast<const T*>(in.p) + t * in.st;
-    T* po = static_cast<T*>(role ? a.c.v : a.c.k) + row * D;
-    const long long osh = static_cast<long long>(page_size) * D;
-    if (role == 1) {
-      each_row<T, T, U>(pi, in.sh, po, osh, in.heads, lane, [](float*) {});
-      continue;
-    }
-    Turn<AXES> turn;
-    if constexpr (AXES > 0) {
-      long long p0 = place, p1 = 0;
-      if (a.pos) {
-        p0 = a.pos[t * AXES];
-        p1 = a.pos[t * AXES + AXES - 1];
+  long long item = static_cast<long long>(blockIdx.x) * WARPS + (threadIdx.x >> 5);
+  const unsigned long long f = lane_freq<AXES>(a.rope, lane);
+  long long end = 0;                                       // first item behind the tensor
+#pragma unroll 1
+  for (int role = PAGED ? 1 : 0; role < 3; ++role) {
+    const Rows in = a.in[role], out = a.out[role];
+    if (in.heads == 0) continue;
+    const int batches = (in.heads + 4 * U - 1) / (4 * U);
+    const long long begin = end;
+    end += tokens * batches;
+    if (item >= end) continue;                             // this warp has none of it
+    Affine<T, NORM> af;
+    if (role < 2) af.load(a.w[role], a.b[role], c0, APART);
+    const T* src = static_cast<const T*>(in.p) + r * in.sh + c0;
+    T* dst = static_cast<T*>(out.p) + r * out.sh + c0;
+#pragma unroll 1
+    for (; item < end; item += step) {
+      Item it;
+      it.at(item - begin, batches, 4 * U, a.n_tokens);
+      const T* pi = src + it.o * in.so + it.t * in.st + it.head * in.sh;
+      Raw8<T> raw[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (it.head + 4 * u + r < in.heads) {
+          raw[u].a.load(pi + 4 * u * in.sh);
+          raw[u].b.load(pi + 4 * u * in.sh + APART);
+        }
       }
-      turn.set(f, p0, p1, lane);
+      int p0 = 0, p1 = 0;
+      long long at;
+      if constexpr (PAGED) {
+        at = paged_row(a, it.t, lane, p0);                 // the token's place in a pool
+        if (at < 0) continue;
+      } else {
+        at = it.o * out.so + it.t * out.st;
+      }
+      T* po = dst + at + it.head * out.sh;
+      Turn<AXES> turn;
+      if (AXES > 0 && role < 2) {
+        if (a.pos) {
+          const int* q = a.pos + it.o * a.pos_so + it.t * AXES;
+          p0 = q[0];
+          if constexpr (AXES == 2) p1 = q[1];
+        }
+        turn.set(f, p0, p1, lane);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (it.head + 4 * u >= in.heads) break;            // the whole warp
+        if (role < 2) {
+          Lane8 x;
+          raw[u].get(x);
+          norm_row<NORM>(x, a.eps);
+          af.apply(x);
+          turn.template apply<1>(x);
+          raw[u].put(x);
+        }
+        if (it.head + 4 * u + r < in.heads) {
+          raw[u].a.store(po + 4 * u * out.sh);
+          raw[u].b.store(po + 4 * u * out.sh + APART);
+        }
+      }
     }
-    each_row<T, T, U>(pi, in.sh, po, osh, in.heads, lane, [&](float* x) {
-      norm_row<NORM>(x, a.eps);
-      af.apply(x);
-      turn.template apply<1>(x);
-    });
   }
 }
 
-int blocks_for(long long tokens, int most) {
-  const long long b = (tokens + WARPS - 1) / WARPS;
+// Gradients: with g the output gradient turned back and h the normalised row,
+// db += g, dw += g h, u = g w, dx = r (u - mean(u) - h mean(u h)) (RMS: without
+// mean(u)).  Blocks are dealt to the tensors by their bytes; a block's weight sums
+// go to its own row of `part`, and a second kernel adds those in a fixed order.
+template <typename T, typename G, int NORM, int AXES>
+__global__ void __launch_bounds__(NTHR, 2) norm_rope_bwd_kernel(const __grid_constant__ NormRopeBwdArgs a) {
+  constexpr int U = 2;
+  constexpr bool NORMED = NORM != NORM_NONE;
+  const int lane = threadIdx.x & 31, r = lane >> 3;
+  const int c0 = Chan<AXES>::first(lane & 7);
+  constexpr int APART = Chan<AXES>::APART;
+  int blk = blockIdx.x, role = 0;
+  while (blk >= a.blocks[role]) blk -= a.blocks[role++];
+  const Rows gin = a.dout[role], gout = a.din[role];
+  const Rows xin = a.in[role < 2 ? role : 0];
+  const int batches = (gin.heads + 4 * U - 1) / (4 * U);
+  const long long items = a.n_outer * a.n_tokens * batches, step = static_cast<long long>(a.blocks[role]) * WARPS;
+  const unsigned long long f = lane_freq<AXES>(a.rope, lane);
+  Affine<T, NORMED ? NORM_RMS : NORM_NONE> af;
+  if (role < 2) af.load(a.w[role], nullptr, c0, APART);
+  Lane8 dw, db;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) dw.v[k] = db.v[k] = both(0.f);
+  const G* pg = static_cast<const G*>(gin.p) + r * gin.sh + c0;
+  const T* px = static_cast<const T*>(xin.p) + r * xin.sh + c0;
+  G* po = static_cast<G*>(gout.p) + r * gout.sh + c0;
+  const bool with_x = NORMED && role < 2;
+
+  Raw8<G> rg[U];
+  Raw8<T> rx[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    rx[u].a.zero();
+    rx[u].b.zero();
+  }
+  int p0 = 0, p1 = 0;
+  Item it;
+  auto load = [&](long long x) {
+    it.at(x, batches, 4 * U, a.n_tokens);
+    const G* g = pg + it.o * gin.so + it.t * gin.st + it.head * gin.sh;
+    const T* p = px + it.o * xin.so + it.t * xin.st + it.head * xin.sh;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      rg[u].a.zero();
+      rg[u].b.zero();
+      if (it.head + 4 * u + r < gin.heads) {
+        rg[u].a.load(g + 4 * u * gin.sh);
+        rg[u].b.load(g + 4 * u * gin.sh + APART);
+        if (with_x) {
+          rx[u].a.load(p + 4 * u * xin.sh);
+          rx[u].b.load(p + 4 * u * xin.sh + APART);
+        }
+      }
+    }
+    if (AXES > 0 && role < 2) {
+      const int* q = a.pos + it.o * a.pos_so + it.t * AXES;
+      p0 = q[0];
+      if constexpr (AXES == 2) p1 = q[1];
+    }
+  };
+  long long item = static_cast<long long>(blk) * WARPS + (threadIdx.x >> 5);
+  bool more = item < items;
+  if (more) load(item);
+#pragma unroll 1
+  while (more) {
+    Raw8<G> ng[U];
+    Raw8<T> nx[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      ng[u] = rg[u];
+      nx[u] = rx[u];
+    }
+    const Item cur = it;
+    const int q0 = p0, q1 = p1;
+    item += step;
+    more = item < items;
+    if (more) load(item);
+    G* p = po + cur.o * gout.so + cur.t * gout.st + cur.head * gout.sh;
+    Turn<AXES> turn;
+    if (role < 2) turn.set(f, q0, q1, lane);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (cur.head + 4 * u >= gin.heads) break;            // the whole warp
+      const bool real = cur.head + 4 * u + r < gin.heads;
+      if (role < 2) {
+        Lane8 d;
+        ng[u].get(d);                                      // zeros where there is no head
+        turn.template apply<-1>(d);
+        if constexpr (NORMED) {
+          Lane8 x;
+          nx[u].get(x);
+          const float rs = norm_row<NORM>(x, a.eps);
+          float2 sh = both(0.f);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            if (real) {
+              db.v[k] = add2(db.v[k], d.v[k]);
+              dw.v[k] = fma2(d.v[k], x.v[k], dw.v[k]);
+            }
+            d.v[k] = mul2(d.v[k], af.w.v[k]);
+            sh = fma2(d.v[k], x.v[k], sh);
+          }
+          const float2 nmh = both(row_sum(sh.x + sh.y) * (-1.f / D));
+          const float mu = NORM == NORM_LAYER ? sum8(d.v[0], d.v[1], d.v[2], d.v[3]) * (-1.f / D) : 0.f;
+          const float2 rr = both(rs), nmu = both(mu);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            float2 v = fma2(x.v[k], nmh, d.v[k]);
+            if constexpr (NORM == NORM_LAYER) v = add2(v, nmu);
+            d.v[k] = mul2(v, rr);
+          }
+        }
+        ng[u].put(d);
+      }
+      if (real) {
+        ng[u].a.store(p + 4 * u * gout.sh);
+        ng[u].b.store(p + 4 * u * gout.sh + APART);
+      }
+    }
+  }
+  if constexpr (NORMED) {
+    if (role == 2 || !a.part) return;
+    __shared__ float sums[WARPS][128];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int ch = c0 + (k & 1) * 2 + (k >> 1) * APART;
+      float2 w = dw.v[k], b = db.v[k];
+#pragma unroll
+      for (int x = 8; x < 32; x <<= 1) {
+        w.x += __shfl_xor_sync(0xffffffffu, w.x, x);
+        w.y += __shfl_xor_sync(0xffffffffu, w.y, x);
+        b.x += __shfl_xor_sync(0xffffffffu, b.x, x);
+        b.y += __shfl_xor_sync(0xffffffffu, b.y, x);
+      }
+      if (r == 0) {
+        sums[threadIdx.x >> 5][ch] = w.x;
+        sums[threadIdx.x >> 5][ch + 1] = w.y;
+        sums[threadIdx.x >> 5][64 + ch] = b.x;
+        sums[threadIdx.x >> 5][64 + ch + 1] = b.y;
+      }
+    }
+    __syncthreads();
+    if (threadIdx.x < 128) {
+      float v = 0.f;
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) v += sums[w][threadIdx.x];
+      a.part[(static_cast<long long>(role) * NORM_BWD_BLOCKS + blk) * 128 + threadIdx.x] = v;
+    }
+  }
+}
+
+// one block per tensor: column c of the blocks' rows [blocks][128], eight interleaved chains
+__global__ void __launch_bounds__(1024) norm_rope_sum_kernel(const __grid_constant__ NormRopeBwdArgs a) {
+  __shared__ float sums[8][128];
+  const int col = threadIdx.x & 127, grp = threadIdx.x >> 7, role = blockIdx.x;
+  float v = 0.f;
+#pragma unroll 4
+  for (int i = grp; i < a.blocks[role]; i += 8) v += a.part[(static_cast<long long>(role) * NORM_BWD_BLOCKS + i) * 128 + col];
+  sums[grp][col] = v;
+  __syncthreads();
+  if (grp == 0) {
+#pragma unroll
+    for (int i = 1; i < 8; ++i) v += sums[i][col];
+    float* out = col < 64 ? a.dw[role] : a.db[role];
+    if (out) out[col & 63] = v;
+  }
+}
+
+int blocks_for(long long items, int most) {
+  const long long b = (items + WARPS - 1) / WARPS;
   return static_cast<int>(b < most ? b : most);
 }
 
@@ -442,48 +540,62 @@ int blocks_for(long long tokens, int most) {
     case 6: CALL(2, 0); break;                                              \
     case 7: CALL(2, 1); break;                                              \
     case 8: CALL(2, 2); break;                                              \
-    default: return cudaErrorInvalidValue;                                  \
-  }
+    default: break;                                                         \
+  }                                                                         \
+  return cudaErrorInvalidValue;
+
+template <typename T, int NORM, int AXES, bool PAGED>
+cudaError_t launch_fwd(const NormRopeArgs& a, cudaStream_t st) {
+  constexpr int PER = 4 * (sizeof(T) == 2 ? 4 : 2);        // heads of an item
+  long long items = 0;
+  for (int i = PAGED ? 1 : 0; i < 3; ++i) items += a.n_outer * a.n_tokens * ((a.in[i].heads + PER - 1) / PER);
+  norm_rope_kernel<T, NORM, AXES, PAGED><<<blocks_for(items, FWD_BLOCKS), NTHR, 0, st>>>(a);
+  return cudaGetLastError();
+}
 
 cudaError_t launch_norm_rope(const NormRopeArgs& a, bool fp32, int norm, int axes, cudaStream_t st) {
-  const dim3 grid(blocks_for(a.n_outer * a.n_tokens, 1 << 16), a.in[2].heads ? 3 : 2);
-#define GSA_CALL(N, A)                                                                                      \
-  (fp32 ? norm_rope_kernel<float, N, A><<<grid, NTHR, 0, st>>>(a)                                           \
-        : norm_rope_kernel<__nv_bfloat16, N, A><<<grid, NTHR, 0, st>>>(a))
+#define GSA_CALL(N, A) return fp32 ? launch_fwd<float, N, A, false>(a, st) : launch_fwd<__nv_bfloat16, N, A, false>(a, st)
   GSA_BY_NORM_AXES(GSA_CALL)
 #undef GSA_CALL
-  return cudaGetLastError();
 }
 
-cudaError_t launch_norm_rope_bwd(const NormRopeBwdArgs& in, bool fp32, bool grad_fp32, int norm, int axes,
-                                 cudaStream_t st) {
-  NormRopeBwdArgs a = in;
-  a.n_part = blocks_for(a.n_outer * a.n_tokens, NORM_BWD_BLOCKS);
-  if (a.n_part > 0) {
-    const dim3 grid(a.n_part, a.dout[2].heads ? 3 : 2);
-#define GSA_CALL(N, A)                                                                                      \
-  (fp32 ? norm_rope_bwd_kernel<float, float, N, A><<<grid, NTHR, 0, st>>>(a)                                \
-        : grad_fp32 ? norm_rope_bwd_kernel<__nv_bfloat16, float, N, A><<<grid, NTHR, 0, st>>>(a)            \
-                    : norm_rope_bwd_kernel<__nv_bfloat16, __nv_bfloat16, N, A><<<grid, NTHR, 0, st>>>(a))
-    GSA_BY_NORM_AXES(GSA_CALL)
-#undef GSA_CALL
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
+template <typename T, typename G, int NORM, int AXES>
+cudaError_t launch_bwd(NormRopeBwdArgs a, cudaStream_t st) {
+  // blocks by each tensor's bytes, at most what has items
+  double bytes[3], all = 0.0;
+  for (int i = 0; i < 3; ++i) {
+    bytes[i] = a.dout[i].heads * (2.0 * sizeof(G) + (i < 2 && NORM != NORM_NONE ? sizeof(T) : 0));
+    all += bytes[i];
   }
-  if (a.part && norm != NORM_NONE)
-    // a tensor that is left out has no sums to write (its pointers are null)
-    norm_rope_sum_kernel<<<2, 1024, 0, st>>>(a.part, a.n_part, a.dw[0], a.db[0], a.dw[1], a.db[1]);
+  int total = 0;
+  for (int i = 0; i < 3; ++i) {
+    a.blocks[i] = 0;
+    const long long items = a.n_outer * a.n_tokens * ((a.dout[i].heads + 7) / 8);
+    if (items == 0) continue;
+    const int share = static_cast<int>(NORM_BWD_BLOCKS * bytes[i] / all);
+    a.blocks[i] = blocks_for(items, share < 1 ? 1 : share);
+    total += a.blocks[i];
+  }
+  if (total > 0) norm_rope_bwd_kernel<T, G, NORM, AXES><<<total, NTHR, 0, st>>>(a);
+  // a tensor that is left out has no sums to write (its pointers are null)
+  if (a.part && NORM != NORM_NONE) norm_rope_sum_kernel<<<2, 1024, 0, st>>>(a);
   return cudaGetLastError();
 }
 
-cudaError_t launch_append(const AppendArgs& a, bool fp32, int norm, int axes, cudaStream_t st) {
-  const dim3 grid(blocks_for(a.n_tokens, 1 << 16), 2);
-#define GSA_CALL(N, A)                                                                                      \
-  (fp32 ? append_kernel<float, N, A><<<grid, NTHR, 0, st>>>(a)                                              \
-        : append_kernel<__nv_bfloat16, N, A><<<grid, NTHR, 0, st>>>(a))
+cudaError_t launch_norm_rope_bwd(const NormRopeBwdArgs& a, bool fp32, bool grad_fp32, int norm, int axes,
+                                 cudaStream_t st) {
+#define GSA_CALL(N, A)                                                              \
+  return fp32 ? launch_bwd<float, float, N, A>(a, st)                               \
+              : grad_fp32 ? launch_bwd<__nv_bfloat16, float, N, A>(a, st)           \
+                          : launch_bwd<__nv_bfloat16, __nv_bfloat16, N, A>(a, st)
   GSA_BY_NORM_AXES(GSA_CALL)
 #undef GSA_CALL
-  return cudaGetLastError();
+}
+
+cudaError_t launch_append(const NormRopeArgs& a, bool fp32, int norm, int axes, cudaStream_t st) {
+#define GSA_CALL(N, A) return fp32 ? launch_fwd<float, N, A, true>(a, st) : launch_fwd<__nv_bfloat16, N, A, true>(a, st)
+  GSA_BY_NORM_AXES(GSA_CALL)
+#undef GSA_CALL
 }
 
 }  // namespace gsa

@@ -79,13 +79,18 @@ int check_op(const gsa_norm_rope* op) {
   return GSA_OK;
 }
 
-// turns per unit of position: base^(-i / half) / (2 pi)
+// turns per unit of position, base^(-i / half) / (2 pi), modulo a turn in 64-bit fixed point:
+// off by 2^-64 and the long double's rounding, so a position of 2^31 by about 2^-33 of a turn
 void make_table(const gsa_norm_rope* op, RopeTable* t) {
   memset(t, 0, sizeof(*t));
   if (op->rope_axes == 0) return;
   const int half = 32 / op->rope_axes;
-  const double two_pi = 6.283185307179586476925;
-  for (int i = 0; i < half; ++i) t->f[i] = pow(op->rope_base, -static_cast<double>(i) / half) / two_pi;
+  const long double two_pi = 6.283185307179586476925286766559L;
+  for (int i = 0; i < half; ++i) {
+    long double f = powl(op->rope_base, -static_cast<long double>(i) / half) / two_pi;
+    f -= floorl(f);
+    t->f[i] = static_cast<unsigned long long>(ldexpl(f, 64));
+  }
 }
 
 // weight and bias of one normed tensor
@@ -264,16 +269,21 @@ extern "C" int gsa_cache_append(const gsa_kv_cache* cache, const gsa_norm_rope* 
   GSA_TRY(check_positions(op, positions, 1, 0, true));
   int* words = nullptr;
   GSA_TRY(status_words(&words));
-  AppendArgs a;
+  NormRopeArgs a;
   memset(&a, 0, sizeof(a));
   a.c = make_cache(cache);
-  a.in[0] = make_rows(k);
-  a.in[1] = make_rows(v);
-  a.w = k_weight;
-  a.b = k_bias;
+  a.in[1] = make_rows(k);
+  a.in[2] = make_rows(v);
+  a.out[1].p = cache->k_pages;
+  a.out[2].p = cache->v_pages;
+  a.out[1].sh = a.out[2].sh = static_cast<long long>(cache->page_size) * D;
+  a.out[1].heads = a.out[2].heads = cache->kv_heads;
+  a.w[1] = k_weight;
+  a.b[1] = k_bias;
   a.cu = cu_tokens;
   a.start = start;
   a.pos = positions;
+  a.n_outer = 1;
   a.n_tokens = n_tokens;
   a.eps = op->eps;
   make_table(op, &a.rope);

@@ -12,10 +12,18 @@ struct Rows {
 };
 
 struct RopeTable {
-  double f[32];              // turns per unit of position of each channel pair
+  unsigned long long f[32];  // turns per unit of position of each channel pair, modulo 1, in 2^-64
 };
 
 enum NormMode : int { NORM_NONE = 0, NORM_LAYER = 1, NORM_RMS = 2 };
+
+// ---- paged cache ------------------------------------------------------------
+struct PagedCache {
+  void *k, *v;               // [num_pages][heads][1 << page_shift][64]
+  const int* table;          // [batch][max_pages]
+  long long table_stride;
+  int num_pages, page_shift, heads, batch, max_pages;
+};
 
 // ---- norm + rotation --------------------------------------------------------
 struct NormRopeArgs {
@@ -27,8 +35,17 @@ struct NormRopeArgs {
   long long n_outer, n_tokens;
   float eps;
   RopeTable rope;
+  // appending to a cache: k (in[1]) and v (in[2]) go to the places of packed tokens
+  // (n_outer 1), out[1] and out[2] being the pools with their head strides
+  PagedCache c;
+  const int *cu, *start;
+  int* err;                  // bounds word
 };
+cudaError_t launch_append(const NormRopeArgs& a, bool fp32, int norm, int axes, cudaStream_t st);
 cudaError_t launch_norm_rope(const NormRopeArgs& a, bool fp32, int norm, int axes, cudaStream_t st);
+
+// blocks of the backward, two per SM (each writes one row of partial sums)
+constexpr int NORM_BWD_BLOCKS = 148 * 2;
 
 struct NormRopeBwdArgs {
   Rows in[2], dout[3], din[3];
@@ -38,35 +55,13 @@ struct NormRopeBwdArgs {
   long long n_outer, n_tokens;
   float eps;
   RopeTable rope;
-  float* part;               // [2][n_part][128]: weight and bias sums of q and k per block
-  int n_part;
+  float* part;               // [2][NORM_BWD_BLOCKS][128]: weight and bias sums of q and k per block
+  int blocks[3];             // blocks of each tensor (set by the launcher)
   float* dw[2];
   float* db[2];
 };
-// blocks per tensor of the backward (each writes one row of partial sums)
-constexpr int NORM_BWD_BLOCKS = 148 * 4;
 cudaError_t launch_norm_rope_bwd(const NormRopeBwdArgs& a, bool fp32, bool grad_fp32, int norm, int axes,
                                  cudaStream_t st);
-
-// ---- paged cache ------------------------------------------------------------
-struct PagedCache {
-  void *k, *v;               // [num_pages][heads][1 << page_shift][64]
-  const int* table;          // [batch][max_pages]
-  long long table_stride;
-  int num_pages, page_shift, heads, batch, max_pages;
-};
-
-struct AppendArgs {
-  PagedCache c;
-  Rows in[2];                // k, v
-  const void *w, *b;
-  const int *cu, *start, *pos;
-  long long n_tokens;
-  float eps;
-  RopeTable rope;
-  int* err;                  // bounds word
-};
-cudaError_t launch_append(const AppendArgs& a, bool fp32, int norm, int axes, cudaStream_t st);
 
 // ---- attention over the paged cache --------------------------------------------
 struct CacheAttnArgs {

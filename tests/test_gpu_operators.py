@@ -235,7 +235,12 @@ def test_norm_rope_backward_parts_places_and_many_rows():
     assert_within("dw", f64(full["dq_weight"]), want[1], (256 + 12000) * U * terms)
     part = gsa.qk_norm_rope_backward(None, x["k"], None, d["k"], None, positions=pos, k_weight=w["k_weight"])
     assert part["dq"] is None and part["dq_weight"] is None and part["dk_bias"] is None
-    assert torch.equal(part["dk"], full["dk"]) and torch.equal(part["dk_weight"], full["dk_weight"])
+    assert torch.equal(part["dk"], full["dk"])
+    # the blocks of the sums depend on the tensors of the call: another order of the same 6,000 terms,
+    # each result within (256 + N) u sum|term| of the exact sum, the two within twice that
+    hk, _ = oo.normed(f64(x["k"]), "layer", 1e-5)
+    terms = (2 * np.abs(f64(d["k"])).max(-1, keepdims=True) * np.abs(hk)).sum((0, 1, 2))
+    assert_within("dk_weight", f64(part["dk_weight"]), f64(full["dk_weight"]), 2 * (256 + 6000) * U * terms)
     # over the output gradients themselves
     dq = d["q"].clone()
     over = gsa.qk_norm_rope_backward(x["q"], None, dq, None, positions=pos, out=(dq, None, None), q_weight=w["q_weight"],
