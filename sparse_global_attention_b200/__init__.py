@@ -337,8 +337,9 @@ class GSALayer:
         ns, F, H = c.num_special, c.num_frames, c.num_heads
         cut = lambda t, s: None if t is None else t[..., s, :]
         if stream is not None:
-            return operators._elsewhere(qkv.device, stream, self.split_qkv_backward, qkv, grads, positions=positions,
-                                        **{n: kw[n] for n in kw if n not in ("head_major", "stream")})
+            kw = {n: kw[n] for n in kw if n not in ("head_major", "stream")}
+            with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=qkv.device)):
+                return self.split_qkv_backward(qkv, grads, positions=positions, **kw)
         d = torch.empty(qkv.shape, dtype=torch.float32, device=qkv.device)
         res = {"dqkv": d}
         for name, at in (("spec", slice(0, ns)), ("img", slice(ns, None))):

@@ -5,7 +5,9 @@
 Each .cu under csrc/ compiles to an object in _build/ (in parallel); the
 objects link into sparse_global_attention_b200/libgsa_b200.so.  Only the CUDA
 runtime is linked (statically, so the library needs nothing at run time but the
-driver).
+driver).  csrc/torch_binding.cpp, the marshalling of torch tensors for the
+operators around the layer, becomes _torch_binding.so beside it (host code
+against the installed torch's headers; it has no kernels).
 """
 from __future__ import annotations
 
@@ -22,6 +24,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libgsa_b200.so")
+BINDING = os.path.join(PKG, "_torch_binding.so")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -30,6 +33,24 @@ def nvcc() -> str:
         if p and os.path.exists(p):
             return p
     raise RuntimeError("nvcc not found: the CUDA toolkit is required to build libgsa_b200.so")
+
+
+def build_binding() -> str:
+    import sysconfig
+
+    from torch.utils import cpp_extension
+    inc = [*cpp_extension.include_paths(), sysconfig.get_paths()["include"],
+           os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")]
+    libs = cpp_extension.library_paths()
+    tmp = BINDING + ".tmp"
+    cmd = [shutil.which("g++") or "g++", "-std=c++17", "-O2", "-fPIC", "-shared", "-fvisibility=hidden", "-w",
+           *[f"-I{d}" for d in inc], os.path.join(CSRC, "torch_binding.cpp"), "-o", tmp,
+           *[f"-L{d}" for d in libs], "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on torch_binding.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+    return BINDING
 
 
 def build(debug: bool = False, verbose: bool = False) -> str:
@@ -52,10 +73,12 @@ def build(debug: bool = False, verbose: bool = False) -> str:
         return obj, r.stderr
 
     with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as ex:
+        binding = ex.submit(build_binding)
         for obj, log in ex.map(one, srcs):
             objs.append(obj)
             if verbose and log:
                 sys.stderr.write(log)
+        binding.result()
     tmp = LIB + ".tmp"
     cmd = [nvcc(), *ARCH, "-shared", "-Xcompiler", "-fPIC", "-cudart", "static", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
