@@ -846,48 +846,100 @@ __global__ void __launch_bounds__(256, 2) cache_attn_f32_kernel(const __grid_con
 }
 
 // ---- joining the splits ---------------------------------------------------------
-// o = sum_s 2^((m_s - m) c) o_s / sum_s 2^((m_s - m) c) l_s.  One warp per row
-// (token, head), two channels per lane; a split that saw no key has l = 0 and no o.
-template <typename T>
+// o = sum_s 2^((m_s - m) c) o_s / sum_s 2^((m_s - m) c) l_s.  Sixteen lanes hold the 64
+// channels of a part; TPR / 16 such groups take a row's parts in turn, each with a
+// running maximum, and are joined at the end.  Few parts: 32 threads a row; many (one
+// token over a long cache): 128, since the parts' loads are what takes the time (one warp
+// with a part at a time took 30 us for 100 parts).  A split that saw no key has l = 0
+// and wrote no o; what lies there is not used.
+template <typename T, int TPR>
 __global__ void __launch_bounds__(128) cache_join_kernel(const __grid_constant__ CacheAttnArgs a) {
-  const int lane = threadIdx.x & 31;
+  constexpr int G = TPR / 16, RPB = 128 / TPR;
+  const int lane = threadIdx.x & 31, sub = threadIdx.x % TPR, g = sub >> 4, e0 = 4 * (sub & 15);
   const long long rows = static_cast<long long>(a.n_tokens) * a.q.heads;
-  const long long row = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  if (row >= rows) return;
-  const int at = static_cast<int>(row / a.q.heads), head = static_cast<int>(row - static_cast<long long>(at) * a.q.heads);
+  const long long row = static_cast<long long>(blockIdx.x) * RPB + threadIdx.x / TPR;
+  bool real = row < rows;
+  const int at = real ? static_cast<int>(row / a.q.heads) : 0;
+  const int head = real ? static_cast<int>(row - static_cast<long long>(at) * a.q.heads) : 0;
   // the row's sequence: rows of none, and of a refused one, stay as they are
-  int lo = 0, hi = a.c.batch;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (a.cu[mid] <= at) lo = mid; else hi = mid;
+  if (real) {
+    int lo = 0, hi = a.c.batch;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (a.cu[mid] <= at) lo = mid; else hi = mid;
+    }
+    real = a.cu[lo] <= at && a.cu[lo + 1] > at && sequence_of(a, lo).ok;
   }
-  if (a.cu[lo] > at || a.cu[lo + 1] <= at) return;
-  if (!sequence_of(a, lo).ok) return;
-  float mx = -INFINITY;
-  for (int s = lane; s < a.n_split; s += 32) {
-    const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + (s * rows + row) * 2);
-    if (ml.y != 0.f) mx = fmaxf(mx, ml.x);
-  }
+  float m = -INFINITY, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (real) {
+    constexpr int B = 4;
+    for (int s0 = g; s0 < a.n_split; s0 += G * B) {
+      float2 ml[B];
+      float4 ov[B];
 #pragma unroll
-  for (int w = 16; w > 0; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
-  const float mu = (mx == -INFINITY) ? 0.f : mx;
-  float l = 0.f, o0 = 0.f, o1 = 0.f;
-#pragma unroll 4
-  for (int s = 0; s < a.n_split; ++s) {
-    const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + (s * rows + row) * 2);
-    if (ml.y == 0.f) continue;
-    const float2 ov = *reinterpret_cast<const float2*>(a.part_o + (s * rows + row) * D + 2 * lane);
-    const float w = ex2((ml.x - mu) * a.scale_log2);
-    l = fmaf(w, ml.y, l);
-    o0 = fmaf(w, ov.x, o0);
-    o1 = fmaf(w, ov.y, o1);
+      for (int b = 0; b < B; ++b) {
+        const int s = min(s0 + b * G, a.n_split - 1);
+        ml[b] = *reinterpret_cast<const float2*>(a.part_ml + (s * rows + row) * 2);
+        ov[b] = *reinterpret_cast<const float4*>(a.part_o + (s * rows + row) * D + e0);
+      }
+#pragma unroll
+      for (int b = 0; b < B; ++b) {
+        if (s0 + b * G >= a.n_split || ml[b].y == 0.f) continue;
+        const float mn = fmaxf(m, ml[b].x), mu = mn == -INFINITY ? 0.f : mn;
+        const float f0 = ex2((m - mu) * a.scale_log2), f1 = ex2((ml[b].x - mu) * a.scale_log2);
+        m = mn;
+        l = fmaf(f1, ml[b].y, f0 * l);
+        o.x = fmaf(f1, ov[b].x, f0 * o.x);
+        o.y = fmaf(f1, ov[b].y, f0 * o.y);
+        o.z = fmaf(f1, ov[b].z, f0 * o.z);
+        o.w = fmaf(f1, ov[b].w, f0 * o.w);
+      }
+    }
   }
+  auto merge = [&](float m1, float l1, float4 o1) {
+    const float mn = fmaxf(m, m1), mu = mn == -INFINITY ? 0.f : mn;
+    const float f0 = ex2((m - mu) * a.scale_log2), f1 = ex2((m1 - mu) * a.scale_log2);
+    m = mn;
+    l = fmaf(f1, l1, f0 * l);
+    o.x = fmaf(f1, o1.x, f0 * o.x);
+    o.y = fmaf(f1, o1.y, f0 * o.y);
+    o.z = fmaf(f1, o1.z, f0 * o.z);
+    o.w = fmaf(f1, o1.w, f0 * o.w);
+  };
+  // the warp's two groups
+  {
+    const float m1 = __shfl_xor_sync(0xffffffffu, m, 16), l1 = __shfl_xor_sync(0xffffffffu, l, 16);
+    float4 o1;
+    o1.x = __shfl_xor_sync(0xffffffffu, o.x, 16);
+    o1.y = __shfl_xor_sync(0xffffffffu, o.y, 16);
+    o1.z = __shfl_xor_sync(0xffffffffu, o.z, 16);
+    o1.w = __shfl_xor_sync(0xffffffffu, o.w, 16);
+    merge(m1, l1, o1);
+  }
+  if constexpr (TPR == 128) {
+    __shared__ float4 so[4][16];
+    __shared__ float2 sml[4];
+    const int w = threadIdx.x >> 5;
+    if (lane < 16) so[w][lane] = o;
+    if (lane == 0) sml[w] = make_float2(m, l);
+    __syncthreads();
+    if (threadIdx.x >= 16) return;
+#pragma unroll
+    for (int k = 1; k < 4; ++k) merge(sml[k].x, sml[k].y, so[k][lane]);
+  } else if (lane >= 16) {
+    return;
+  }
+  if (!real) return;
   const float inv = l > 0.f ? 1.f / l : (l == l ? 0.f : l);
-  T* out = static_cast<T*>(a.out.p) + at * a.out.st + head * a.out.sh + 2 * lane;
-  if constexpr (sizeof(T) == 2) *reinterpret_cast<uint32_t*>(out) = pack_bf16(o0 * inv, o1 * inv);
-  else *reinterpret_cast<float2*>(out) = make_float2(o0 * inv, o1 * inv);
-  if (a.lse && lane == 0)
-    a.lse[static_cast<long long>(head) * a.n_tokens + at] = l == 0.f ? -INFINITY : (mu * a.scale_log2 + log2f(l)) * LN2;
+  T* out = static_cast<T*>(a.out.p) + at * a.out.st + head * a.out.sh + e0;
+  if constexpr (sizeof(T) == 2)
+    *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+  else
+    *reinterpret_cast<float4*>(out) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+  if (a.lse && e0 == 0)
+    a.lse[static_cast<long long>(head) * a.n_tokens + at] =
+        l == 0.f ? -INFINITY : (m * a.scale_log2 + log2f(l)) * LN2;
 }
 
 // ---- host -------------------------------------------------------------------------
@@ -945,57 +997,49 @@ CacheAttnPlan plan_cache_attn(bool fp32, int batch, int kv_heads, int q_heads, l
   CacheAttnPlan p;
   const long long most = n_tokens < max_new ? n_tokens : max_new;
   const long long rows = most * (q_heads / kv_heads);
-  // rows and keys per tile, rows that a block counts in, blocks that run at once, key tiles
-  // worth a split, key tiles that a block's start costs
-  int tile, keys, unit, slots, least;
-  double start;
-  if (fp32) {
-    p.kind = rows <= 16 ? F32_16 : F32_64;
-    tile = unit = rows <= 16 ? 16 : 64;
-    keys = FK;
-    slots = 296;
-    least = 2;
-    start = 0.3;
-  } else if (rows <= 32) {
-    p.kind = QUARTERS;
-    tile = unit = 32;
-    keys = Lay<QUARTERS>::TK;
-    slots = 296;
-    least = 4;
-    start = 1;
-  } else if (rows <= 128) {
-    p.kind = ONE_TILE;
-    tile = unit = 128;
-    keys = Lay<ONE_TILE>::TK;
-    slots = 148;
-    least = 4;
-    start = 2;
-  } else {
-    p.kind = ROW_TILES;
-    tile = Lay<ROW_TILES>::ROWS;
-    unit = 128;
-    keys = Lay<ROW_TILES>::TK;
-    slots = 148;
-    least = 16;
-    start = 3;
-  }
-  p.row_tiles = static_cast<int>((rows + tile - 1) / tile);
+  // Per variant: rows and keys of a tile, blocks that run at once, key tiles worth a split, and
+  // measured times in us: a key tile of a block alone and with all SMs at work, a block's start.
+  struct Cost {
+    int tile, keys, slots, least;
+    double alone, busy, start;
+  };
+  static const Cost costs[] = {{256, 128, 148, 16, 1.4, 1.4, 4.0},       // ROW_TILES
+                               {128, 128, 148, 2, 0.75, 0.75, 5.0},      // ONE_TILE
+                               {32, 128, 296, 2, 0.55, 1.5, 4.0},        // QUARTERS
+                               {64, 64, 296, 2, 2.2, 4.2, 6.0},          // F32_64
+                               {16, 64, 296, 2, 0.9, 1.6, 3.0}};         // F32_16
+  p.kind = fp32 ? (rows <= 16 ? F32_16 : F32_64) : (rows <= 32 ? QUARTERS : rows <= 128 ? ONE_TILE : ROW_TILES);
+  const Cost& c = costs[p.kind];
+  p.row_tiles = static_cast<int>((rows + c.tile - 1) / c.tile);
   if (p.row_tiles < 1) p.row_tiles = 1;
-  const long long heads = static_cast<long long>(batch) * kv_heads;
-  const long long ktiles = (max_len + keys - 1) / keys;
-  long long ns = 1, most_splits = ktiles / least;
+  const long long ktiles = (max_len + c.keys - 1) / c.keys;
+  long long ns = 1, most_splits = ktiles / c.least;
   if (most_splits > 128) most_splits = 128;
   if (most_splits > 1) {
-    // Rounds that the blocks take on the GPU in units of one unsplit block (a block with one of
-    // its two row tiles counts less), with the cost of a block's start and of joining its part
-    // as some key tiles more.
-    const long long units = (rows + unit - 1) / unit;
-    // a block with one of its two row tiles takes four fifths of the time
-    const double load = heads * (units / (tile / unit) + (units % (tile / unit) ? 0.8 : 0.0)) / slots;
+    // The blocks that have rows (a block with one of its two row tiles takes four fifths of the
+    // time), and of their keys what several sequences of different lengths have on average: the
+    // lengths are on the device.
+    const int half = p.kind == ROW_TILES ? 2 : 1;
+    const double group = static_cast<double>(q_heads) / kv_heads;
+    const long long units = (rows * half + c.tile - 1) / c.tile;
+    double blocks = static_cast<double>(units / half) + (units % half ? 0.8 : 0.0);
+    if (batch > 1 && n_tokens * group / c.tile + 0.5 * batch < blocks * batch)
+      blocks = n_tokens * group / c.tile + 0.5 * batch;
+    else
+      blocks *= batch;
+    blocks *= kv_heads;
+    const double mean = batch > 1 ? 0.6 : 1.0;
     double best = 1e30;
-    for (long long n = 1; n <= most_splits && (n == 1 || load < 2.0) && (n - 1) * load < 4.0; ++n) {
-      const double t = ceil(load * n) / n + start * n / ktiles;
-      if (t < best * 0.99) {
+    for (long long n = 1; n <= most_splits; ++n) {
+      const double chunk = ceil(static_cast<double>(ktiles) / n);
+      const double run = blocks * (mean * n + (n > 1 ? 0.5 * (1.0 - mean) : 1.0 - mean));       // blocks with keys
+      const double r = run / c.slots;
+      const double rounds = r <= 1.0 ? 1.0 : batch > 1 ? r + 0.5 : ceil(r);
+      const double tile_us = c.alone + (c.busy - c.alone) * (r < 1.0 ? r : 1.0);
+      // joining: a launch, and the parts written and read once
+      const double join = n > 1 ? 3.0 + n * n_tokens * q_heads * 1.2e-4 : 0.0;
+      const double t = rounds * (chunk * tile_us + 0.5 * c.start) + 0.5 * c.start + join;
+      if (t < best * 0.95) {
         best = t;
         ns = n;
       }
@@ -1020,9 +1064,15 @@ cudaError_t launch_cache_attn(const CacheAttnArgs& a, bool fp32, int kind, cudaS
   }
   if (e != cudaSuccess || a.n_split == 1) return e;
   const long long rows = static_cast<long long>(a.n_tokens) * a.q.heads;
-  const unsigned grid = static_cast<unsigned>((rows + 3) / 4);
-  if (fp32) cache_join_kernel<float><<<grid, 128, 0, st>>>(a);
-  else cache_join_kernel<__nv_bfloat16><<<grid, 128, 0, st>>>(a);
+  if (a.n_split > 8) {
+    const unsigned grid = static_cast<unsigned>(rows);
+    if (fp32) cache_join_kernel<float, 128><<<grid, 128, 0, st>>>(a);
+    else cache_join_kernel<__nv_bfloat16, 128><<<grid, 128, 0, st>>>(a);
+  } else {
+    const unsigned grid = static_cast<unsigned>((rows + 3) / 4);
+    if (fp32) cache_join_kernel<float, 32><<<grid, 128, 0, st>>>(a);
+    else cache_join_kernel<__nv_bfloat16, 32><<<grid, 128, 0, st>>>(a);
+  }
   return cudaGetLastError();
 }
 
