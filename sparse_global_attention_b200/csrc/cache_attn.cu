@@ -212,15 +212,16 @@ __device__ __forceinline__ Block block_of(const CacheAttnArgs& a) {
   k.h = x % a.c.heads;
   x /= a.c.heads;
   k.b = x % a.c.batch;
-  // with a causal mask a sequence's last tile has the most keys: it starts first
-  const int tile = a.causal ? a.row_tiles - 1 - static_cast<int>(x / a.c.batch) : static_cast<int>(x / a.c.batch);
+  int tile = static_cast<int>(x / a.c.batch);
   k.seq = sequence_of(a, k.b);
   const long long room = static_cast<long long>(a.c.max_pages) << a.c.page_shift;
   k.len = static_cast<int>(min(static_cast<long long>(k.seq.len), room));
   if (threadIdx.x == 0 && (!k.seq.ok || (k.len != k.seq.len && k.seq.n > 0))) set_error(a.err, ERR_BOUNDS);
   k.rows = k.seq.ok ? k.seq.n * a.group : 0;
+  // with a causal mask a sequence's last tile has the most keys: every sequence's last one starts first
+  if (a.causal) tile = (k.rows + TROWS - 1) / TROWS - 1 - tile;
   k.row0 = tile * TROWS;
-  k.any = k.row0 < k.rows;
+  k.any = tile >= 0 && k.row0 < k.rows;
   k.t_begin = k.ntile = 0;
   if (k.any) {
     const int last = min(k.row0 + TROWS, k.rows) - 1;
@@ -243,6 +244,11 @@ __device__ __forceinline__ int row_limit(const CacheAttnArgs& a, const Block& k,
 __device__ __forceinline__ int page_of(const CacheAttnArgs& a, int raw) {
   return raw >= 0 && raw < a.c.num_pages ? raw : -1;
 }
+
+// The join kernel of a split call is launched while the blocks that write the parts still run
+// (programmatic dependent launch): they allow it when they start, it waits for their end.
+__device__ __forceinline__ void allow_join() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
+__device__ __forceinline__ void wait_for_parts() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
 
 // a row's result: normalised output and log-sum-exp, or this split's part
 template <int N>
@@ -282,6 +288,7 @@ __global__ void __launch_bounds__(Lay<KIND>::NTHREADS, KIND == QUARTERS ? 2 : 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::SLOT);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
+  allow_join();
   const Block blk = block_of<L::ROWS, TN>(a);
   if (!blk.any) return;
   if (sbase & 1023u) {                            // the operands' swizzle needs it
@@ -309,29 +316,49 @@ __global__ void __launch_bounds__(Lay<KIND>::NTHREADS, KIND == QUARTERS ? 2 : 1)
     info[L::NST] = 0;
     fence_mbar_init();
   }
+  const int page_size = 1 << a.c.page_shift;
+  const int box = min(page_size, TN);             // rows of one copy
+  const int box_shift = min(a.c.page_shift, 7);
+  const int nbox = TN >> box_shift;
+
+  // The first global loads start before the barrier of the block: the producer's table entries
+  // (lanes 0-7 copy a tile's boxes of K, lanes 8-15 those of V), the softmax warps' rows of Q.
+  const int* table = a.c.table + blk.b * a.c.table_stride;
+  const int my = lane & 7;
+  const bool mine = lane < 16 && my < nbox;
+  auto slot_of = [&](int it) { return (blk.t_begin + it) * TN + (my << box_shift); };
+  auto lookup = [&](int it) {
+    const int slot = slot_of(it);
+    return mine && it < ntile && slot < blk.len ? table[slot >> a.c.page_shift] : -1;
+  };
+  constexpr bool QUAD = L::QUAD;
+  constexpr int CH = 8 / L::HALVES;               // 16-byte chunks of Q: each warp of a pair one half of a row
+  const int stream = warp / L::TWARP;
+  const int half = QUAD ? 0 : (warp >> 2) & 1;
+  const int r = threadIdx.x & 127;                // row in the tile = TMEM lane
+  const int row = blk.row0 + (QUAD ? lane : (L::R > 1 ? stream * TM : 0) + r);
+  const bool real = warp < L::NWARP && row < blk.rows;
+  const int token = real ? row / a.group : 0;
+  const int head = blk.h * a.group + (real ? row - token * a.group : 0);
+  const int at = blk.seq.first + token;
+  int first_page = -1;
+  uint4 qrow[CH];
+  if (warp == L::NWARP) first_page = lookup(0);
+  if (warp < L::NWARP && (L::R > 1 || stream == 0)) {
+    const uint4* src = reinterpret_cast<const uint4*>(
+        static_cast<const __nv_bfloat16*>(a.q.p) + at * a.q.st + head * a.q.sh) + CH * half;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) qrow[c] = real ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+  }
   if (warp == 0) tmem_alloc<L::COLS>(smem_u32(tmem_slot));
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  const int page_size = 1 << a.c.page_shift;
-  const int box = min(page_size, TN);             // rows of one copy
-  const int box_shift = min(a.c.page_shift, TN == 128 ? 7 : 6);
-  const int nbox = TN >> box_shift;
-
   if (warp == L::NWARP) {
     // ------------------------------------------------------------ TMA producer
-    // lanes 0-7 copy the tile's boxes of K, lanes 8-15 those of V
-    const int* table = a.c.table + blk.b * a.c.table_stride;
-    const int my = lane & 7;
-    const bool mine = lane < 16 && my < nbox;
-    auto slot_of = [&](int it) { return (blk.t_begin + it) * TN + (my << box_shift); };
-    auto lookup = [&](int it) {
-      const int slot = slot_of(it);
-      return mine && it < ntile && slot < blk.len ? table[slot >> a.c.page_shift] : -1;
-    };
-    int next = lookup(0);
+    int next = first_page;
     int issued = 0;
     for (int it = 0; it < ntile; ++it) {
       const int s = it % L::NST;
@@ -435,21 +462,13 @@ __global__ void __launch_bounds__(Lay<KIND>::NTHREADS, KIND == QUARTERS ? 2 : 1)
     }
   } else if (warp < L::TWARP * nstream) {
     // ------------------------------------------------------------ softmax
-    constexpr bool QUAD = L::QUAD;
     constexpr int NC = QUAD ? 1 : 2;               // 32-key chunks of a tile that a thread takes
-    const int i = warp / L::TWARP;                 // stream
-    const int half = QUAD ? 0 : (warp >> 2) & 1;
+    const int i = stream;
     const int first = L::R > 1 ? 0 : i;
     const int count = first < ntile ? (ntile - first + L::STEP - 1) / L::STEP : 0;
     const int c0 = QUAD ? 32 * warp : 64 * half;   // first of its keys
-    const int r = threadIdx.x & 127;               // row in the tile = TMEM lane
     const int pair_bar = 2 + (warp & 3) + 4 * i;   // both warps of these 32 rows
     float* xch = reinterpret_cast<float*>(smem + L::XCH) + i * TM + r;
-    const int row = blk.row0 + (QUAD ? lane : (L::R > 1 ? i * TM : 0) + r);
-    const bool real = row < blk.rows;
-    const int token = real ? row / a.group : 0;
-    const int head = blk.h * a.group + (real ? row - token * a.group : 0);
-    const int at = blk.seq.first + token;
     const int lim = real ? row_limit(a, blk, token) : 0x7fffffff;    // rows without a query need no mask
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + lane_off + TN * i + c0;
@@ -458,15 +477,9 @@ __global__ void __launch_bounds__(Lay<KIND>::NTHREADS, KIND == QUARTERS ? 2 : 1)
     const float sl2 = a.scale_log2;
     if (L::R > 1 || i == 0) {
       // this row of Q, into the 128-byte swizzle of the operand
-      constexpr int CH = 8 / L::HALVES;            // each warp of a pair one half of it
-      uint4 w[CH];
-      const uint4* src = reinterpret_cast<const uint4*>(
-          static_cast<const __nv_bfloat16*>(a.q.p) + at * a.q.st + head * a.q.sh) + CH * half;
-#pragma unroll
-      for (int c = 0; c < CH; ++c) w[c] = real ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
 #pragma unroll
       for (int c = 0; c < CH; ++c)
-        *reinterpret_cast<uint4*>(smem + (L::R > 1 ? i : 0) * QTILE + swz(r, CH * half + c)) = w[c];
+        *reinterpret_cast<uint4*>(smem + (L::R > 1 ? i : 0) * QTILE + swz(r, CH * half + c)) = qrow[c];
       if constexpr (QUAD) {
         // P of the other quarters' keys stays zero
         uint32_t z[32];
@@ -693,6 +706,7 @@ __global__ void __launch_bounds__(256, 2) cache_attn_f32_kernel(const __grid_con
   float* sk = reinterpret_cast<float*>(smem + L::K);
   float* sv = reinterpret_cast<float*>(smem + L::V);
   int* skey = reinterpret_cast<int*>(smem + L::OK);
+  allow_join();
   const Block blk = block_of<TR, FK>(a);
   if (!blk.any) return;
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
@@ -872,6 +886,7 @@ __global__ void __launch_bounds__(128) cache_join_kernel(const __grid_constant__
   }
   float m = -INFINITY, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  wait_for_parts();
   if (real) {
     constexpr int B = 4;
     for (int s0 = g; s0 < a.n_split; s0 += G * B) {
@@ -981,6 +996,20 @@ cudaError_t launch_tc(const CacheAttnArgs& a, unsigned blocks, cudaStream_t st) 
   return cudaGetLastError();
 }
 
+cudaError_t launch_join(void (*kernel)(CacheAttnArgs), const CacheAttnArgs& a, long long blocks, cudaStream_t st) {
+  cudaLaunchAttribute early;
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t c;
+  memset(&c, 0, sizeof(c));
+  c.gridDim = dim3(static_cast<unsigned>(blocks));
+  c.blockDim = dim3(128);
+  c.stream = st;
+  c.attrs = &early;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, kernel, a);
+}
+
 template <int TR>
 cudaError_t launch_f32(const CacheAttnArgs& a, unsigned blocks, cudaStream_t st) {
   static std::atomic<unsigned long long> done{0};
@@ -1064,16 +1093,11 @@ cudaError_t launch_cache_attn(const CacheAttnArgs& a, bool fp32, int kind, cudaS
   }
   if (e != cudaSuccess || a.n_split == 1) return e;
   const long long rows = static_cast<long long>(a.n_tokens) * a.q.heads;
-  if (a.n_split > 8) {
-    const unsigned grid = static_cast<unsigned>(rows);
-    if (fp32) cache_join_kernel<float, 128><<<grid, 128, 0, st>>>(a);
-    else cache_join_kernel<__nv_bfloat16, 128><<<grid, 128, 0, st>>>(a);
-  } else {
-    const unsigned grid = static_cast<unsigned>((rows + 3) / 4);
-    if (fp32) cache_join_kernel<float, 32><<<grid, 128, 0, st>>>(a);
-    else cache_join_kernel<__nv_bfloat16, 32><<<grid, 128, 0, st>>>(a);
-  }
-  return cudaGetLastError();
+  if (a.n_split > 8)
+    return fp32 ? launch_join(cache_join_kernel<float, 128>, a, rows, st)
+                : launch_join(cache_join_kernel<__nv_bfloat16, 128>, a, rows, st);
+  return fp32 ? launch_join(cache_join_kernel<float, 32>, a, (rows + 3) / 4, st)
+              : launch_join(cache_join_kernel<__nv_bfloat16, 32>, a, (rows + 3) / 4, st);
 }
 
 }  // namespace gsa
