@@ -31,7 +31,8 @@
 // token, pages that do not exist) are zeroed in shared memory before the product,
 // since 0 * NaN is NaN; scores of such keys are replaced, not added to.
 //
-// fp32 is a register-tiled kernel (64 or 16 rows by 64 keys) with the same split.
+// fp32 runs on the FMA pipe with the same splits: 64 rows by 64 keys per step through shared
+// memory, or, with few rows, warps that stream keys and values through registers.
 //
 // All mbarrier waits are bounded; one that runs out records GSA_ERR_DEVICE_TIMEOUT.
 #include <atomic>
@@ -56,7 +57,7 @@ constexpr float RESCALE_LOG2 = 8.f;      // rescale O when the max grows by > 2^
 constexpr int FMA_PAIRS = 3;              // of 16 pairs of a tile's exponentials, on the FMA pipe
 constexpr float LN2 = 0.6931471805599453f;
 // kernel variants
-enum Kind : int { ROW_TILES = 0, ONE_TILE = 1, QUARTERS = 2, F32_64 = 3, F32_16 = 4 };
+enum Kind : int { ROW_TILES = 0, ONE_TILE = 1, QUARTERS = 2, F32_64 = 3, F32_8 = 4, F32_4 = 5 };
 
 template <int KIND>
 struct Lay {
@@ -682,11 +683,27 @@ __global__ void __launch_bounds__(Lay<KIND>::NTHREADS, KIND == QUARTERS ? 2 : 1)
 }
 
 // ---- fp32 ---------------------------------------------------------------------
-// TR rows by 64 keys per step, 256 threads as 16 x 16: thread (ty, tx) holds
-// TR / 16 rows by 4 keys (tx + 16 i) of S and the same rows by channels 4 tx .. of O.
+// 64 rows by 64 keys per step, 256 threads as 16 x 16: thread (ty, tx) holds 4 rows by
+// 4 keys (tx + 16 i) of S and the same rows by channels 4 tx .. of O.
 constexpr int FK = 64;                    // keys per tile
 constexpr int FP = 68;                    // row pitch in floats: 16-byte reads of 16 rows meet no bank twice
-template <int TR>
+constexpr int TR = 64;
+// four channels of a row's result, or of this split's part
+__device__ __forceinline__ void write_f32(const CacheAttnArgs& a, const Block& blk, int at, int head, int e0, float4 o,
+                                          float m, float l) {
+  if (a.n_split == 1) {
+    const float inv = l > 0.f ? 1.f / l : (l == l ? 0.f : l);        // a NaN stays one
+    *reinterpret_cast<float4*>(static_cast<float*>(a.out.p) + at * a.out.st + head * a.out.sh + e0) =
+        make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+    if (a.lse && e0 == 0)
+      a.lse[static_cast<long long>(head) * a.n_tokens + at] = l == 0.f ? -INFINITY : (m * a.scale_log2 + log2f(l)) * LN2;
+  } else {
+    const long long pr = (static_cast<long long>(blk.split) * a.n_tokens + at) * a.q.heads + head;
+    if (blk.ntile > 0) *reinterpret_cast<float4*>(a.part_o + pr * D + e0) = o;
+    if (e0 == 0) *reinterpret_cast<float2*>(a.part_ml + pr * 2) = make_float2(m, l);
+  }
+}
+
 struct FLay {
   static constexpr int Q = 0;
   static constexpr int K = Q + TR * FP * 4;               // two buffers of K, two of V
@@ -696,9 +713,8 @@ struct FLay {
   static constexpr int BYTES = OK + 2 * FK * 4;
 };
 
-template <int TR>
 __global__ void __launch_bounds__(256, 2) cache_attn_f32_kernel(const __grid_constant__ CacheAttnArgs a) {
-  using L = FLay<TR>;
+  using L = FLay;
   constexpr int R = TR / 16;
   extern __shared__ __align__(1024) uint8_t smem[];
   float* sq = reinterpret_cast<float*>(smem + L::Q);
@@ -843,20 +859,147 @@ __global__ void __launch_bounds__(256, 2) cache_attn_f32_kernel(const __grid_con
     if (row >= blk.rows) continue;
     const int token = row / a.group, head = blk.h * a.group + row - token * a.group;
     const int at = blk.seq.first + token;
-    if (a.n_split == 1) {
-      const float inv = l[i] > 0.f ? 1.f / l[i] : (l[i] == l[i] ? 0.f : l[i]);
-      *reinterpret_cast<float4*>(static_cast<float*>(a.out.p) + at * a.out.st + head * a.out.sh + 4 * tx) =
-          make_float4(o[i][0] * inv, o[i][1] * inv, o[i][2] * inv, o[i][3] * inv);
-      if (a.lse && tx == 0)
-        a.lse[static_cast<long long>(head) * a.n_tokens + at] =
-            l[i] == 0.f ? -INFINITY : (m[i] * a.scale_log2 + log2f(l[i])) * LN2;
-    } else {
-      const long long pr = (static_cast<long long>(blk.split) * a.n_tokens + at) * a.q.heads + head;
-      if (blk.ntile > 0)
-        *reinterpret_cast<float4*>(a.part_o + pr * D + 4 * tx) = make_float4(o[i][0], o[i][1], o[i][2], o[i][3]);
-      if (tx == 0) *reinterpret_cast<float2*>(a.part_ml + pr * 2) = make_float2(m[i], l[i]);
+    write_f32(a, blk, at, head, 4 * tx, make_float4(o[i][0], o[i][1], o[i][2], o[i][3]), m[i], l[i]);
+  }
+}
+
+// Few rows: bound by reading the cache.  A warp streams steps of N x 2 keys on its own: a half-warp
+// holds a key's 64 channels, four per lane, as loaded from memory; a row's scores of a step are
+// partial products of each lane, summed and dealt out over the 16 lanes in one exchange (N values:
+// 8 shuffles for 8 keys), so that lane c ends with the score of key 2 (c / (16 / N)) + half; the
+// weights are handed back by shuffles for O += p V.  Each warp has its own running maximum and
+// sums; the block's eight warps are joined at the end.  A step's keys lie in one page.  16 rows by
+// 64 keys through shared memory (one row a thread) read 1.6 TB/s where this reads FEW_TBS.
+template <int R, int N>
+__global__ void __launch_bounds__(256, 2) cache_attn_f32_few_kernel(const __grid_constant__ CacheAttnArgs a) {
+  constexpr int KEYS = 2 * N, WARPS = 8, PART = 66;
+  __shared__ float parts[WARPS][R][PART];
+  allow_join();
+  const Block blk = block_of<R, FK>(a);
+  if (!blk.any) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, half = lane >> 4, c = lane & 15;
+  const int page_size = 1 << a.c.page_shift;
+  const int* table = a.c.table + blk.b * a.c.table_stride;
+  float4 q[R], o[R];
+  float m[R], l[R];
+  int lim[R];
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const int row = blk.row0 + i;
+    o[i] = q[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    m[i] = -INFINITY;
+    l[i] = 0.f;
+    lim[i] = 0;
+    if (row < blk.rows) {
+      const int token = row / a.group, head = blk.h * a.group + row - token * a.group;
+      q[i] = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(a.q.p) +
+                                                   (blk.seq.first + token) * a.q.st + head * a.q.sh) + c);
+      lim[i] = row_limit(a, blk, token);
     }
   }
+  const int k0 = blk.t_begin * FK, k1 = min((blk.t_begin + blk.ntile) * FK, blk.len);
+  int raw = k0 + warp * KEYS < k1 ? __ldg(table + ((k0 + warp * KEYS) >> a.c.page_shift)) : -1;
+  for (int kb = k0 + warp * KEYS; kb < k1; kb += WARPS * KEYS) {
+    const int page = page_of(a, raw);
+    if (page < 0 && lane == 0) set_error(a.err, ERR_BOUNDS);
+    const int after = kb + WARPS * KEYS;
+    if (after < k1) raw = __ldg(table + (after >> a.c.page_shift));
+    const long long row =
+        ((static_cast<long long>(max(page, 0)) * a.c.heads + blk.h) << a.c.page_shift) + (kb & (page_size - 1)) + half;
+    const float4* pk = reinterpret_cast<const float4*>(static_cast<const float*>(a.c.k) + row * D) + c;
+    const float4* pv = reinterpret_cast<const float4*>(static_cast<const float*>(a.c.v) + row * D) + c;
+    float4 k[N], v[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const bool there = page >= 0 && kb + 2 * i + half < blk.len;
+      k[i] = there ? __ldg(pk + 32 * i) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const bool there = page >= 0 && kb + 2 * i + half < blk.len;
+      v[i] = there ? __ldg(pv + 32 * i) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    const int key = kb + 2 * (c / (16 / N)) + half;          // whose score this lane ends with
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      if (i > 0 && blk.row0 + i >= blk.rows) break;          // the whole block
+      float s[N];
+#pragma unroll
+      for (int e = 0; e < N; ++e)
+        s[e] = fmaf(q[i].x, k[e].x, fmaf(q[i].y, k[e].y, fmaf(q[i].z, k[e].z, q[i].w * k[e].w)));
+      // sum over the half-warp's lanes; each exchange halves the values that a lane keeps
+      int x = 8;
+#pragma unroll
+      for (int n = N / 2; n > 0; n >>= 1, x >>= 1) {
+        const bool up = (c & x) != 0;
+#pragma unroll
+        for (int e = 0; e < n; ++e) {
+          const float give = up ? s[e] : s[e + n];
+          s[e] = (up ? s[e + n] : s[e]) + __shfl_xor_sync(0xffffffffu, give, x);
+        }
+      }
+      for (; x > 0; x >>= 1) s[0] += __shfl_xor_sync(0xffffffffu, s[0], x);
+      float sc = page >= 0 && key < lim[i] ? s[0] : -INFINITY;
+      float mx = sc;
+#pragma unroll
+      for (int w = 16 / N; w < 32; w <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
+      const float mn = fmaxf(m[i], mx), mu = mn == -INFINITY ? 0.f : mn;
+      const float alpha = exp2f((m[i] - mu) * a.scale_log2);
+      const float p = exp2f((sc - mu) * a.scale_log2);
+      m[i] = mn;
+      l[i] = fmaf(l[i], alpha, p);
+      o[i].x *= alpha;
+      o[i].y *= alpha;
+      o[i].z *= alpha;
+      o[i].w *= alpha;
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        const float pe = __shfl_sync(0xffffffffu, p, (half << 4) | (e * (16 / N)));
+        o[i].x = fmaf(pe, v[e].x, o[i].x);
+        o[i].y = fmaf(pe, v[e].y, o[i].y);
+        o[i].z = fmaf(pe, v[e].z, o[i].z);
+        o[i].w = fmaf(pe, v[e].w, o[i].w);
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    // the two halves' sums of O; l over the lanes of different keys
+    o[i].x += __shfl_xor_sync(0xffffffffu, o[i].x, 16);
+    o[i].y += __shfl_xor_sync(0xffffffffu, o[i].y, 16);
+    o[i].z += __shfl_xor_sync(0xffffffffu, o[i].z, 16);
+    o[i].w += __shfl_xor_sync(0xffffffffu, o[i].w, 16);
+#pragma unroll
+    for (int w = 16 / N; w < 32; w <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], w);
+    if (half == 0) {
+      float* p = parts[warp][i] + 4 * c;
+      p[0] = o[i].x;
+      p[1] = o[i].y;
+      p[2] = o[i].z;
+      p[3] = o[i].w;
+    }
+    if (lane == 0) {
+      parts[warp][i][64] = m[i];
+      parts[warp][i][65] = l[i];
+    }
+  }
+  __syncthreads();
+  const int i = threadIdx.x >> 4, e0 = 4 * (threadIdx.x & 15), row = blk.row0 + i;
+  if (i >= R || row >= blk.rows) return;
+  float mx = -INFINITY;
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) mx = fmaxf(mx, parts[w][i][64]);
+  const float mu = mx == -INFINITY ? 0.f : mx;
+  float ls = 0.f, os[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) {
+    const float f = exp2f((parts[w][i][64] - mu) * a.scale_log2);
+    ls = fmaf(f, parts[w][i][65], ls);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) os[e] = fmaf(f, parts[w][i][e0 + e], os[e]);
+  }
+  const int token = row / a.group, head = blk.h * a.group + row - token * a.group;
+  write_f32(a, blk, blk.seq.first + token, head, e0, make_float4(os[0], os[1], os[2], os[3]), mx, ls);
 }
 
 // ---- joining the splits ---------------------------------------------------------
@@ -1010,12 +1153,11 @@ cudaError_t launch_join(void (*kernel)(CacheAttnArgs), const CacheAttnArgs& a, l
   return cudaLaunchKernelEx(&c, kernel, a);
 }
 
-template <int TR>
 cudaError_t launch_f32(const CacheAttnArgs& a, unsigned blocks, cudaStream_t st) {
   static std::atomic<unsigned long long> done{0};
-  cudaError_t e = allow_smem(cache_attn_f32_kernel<TR>, FLay<TR>::BYTES, done);
+  cudaError_t e = allow_smem(cache_attn_f32_kernel, FLay::BYTES, done);
   if (e != cudaSuccess) return e;
-  cache_attn_f32_kernel<TR><<<blocks, 256, FLay<TR>::BYTES, st>>>(a);
+  cache_attn_f32_kernel<<<blocks, 256, FLay::BYTES, st>>>(a);
   return cudaGetLastError();
 }
 
@@ -1036,8 +1178,9 @@ CacheAttnPlan plan_cache_attn(bool fp32, int batch, int kv_heads, int q_heads, l
                                {128, 128, 148, 2, 0.75, 0.75, 5.0},      // ONE_TILE
                                {32, 128, 296, 2, 0.55, 1.5, 4.0},        // QUARTERS
                                {64, 64, 296, 2, 2.2, 4.2, 6.0},          // F32_64
-                               {16, 64, 296, 2, 0.9, 1.6, 3.0}};         // F32_16
-  p.kind = fp32 ? (rows <= 16 ? F32_16 : F32_64) : (rows <= 32 ? QUARTERS : rows <= 128 ? ONE_TILE : ROW_TILES);
+                               {8, 64, 296, 2, 0.5, 1.5, 3.0},           // F32_8
+                               {4, 64, 296, 2, 0.4, 1.5, 3.0}};          // F32_4
+  p.kind = fp32 ? (rows <= 4 ? F32_4 : rows <= 24 ? F32_8 : F32_64) : (rows <= 32 ? QUARTERS : rows <= 128 ? ONE_TILE : ROW_TILES);
   const Cost& c = costs[p.kind];
   p.row_tiles = static_cast<int>((rows + c.tile - 1) / c.tile);
   if (p.row_tiles < 1) p.row_tiles = 1;
@@ -1087,8 +1230,15 @@ cudaError_t launch_cache_attn(const CacheAttnArgs& a, bool fp32, int kind, cudaS
     case ROW_TILES: e = launch_tc<ROW_TILES>(a, blocks, st); break;
     case ONE_TILE: e = launch_tc<ONE_TILE>(a, blocks, st); break;
     case QUARTERS: e = launch_tc<QUARTERS>(a, blocks, st); break;
-    case F32_64: e = launch_f32<64>(a, blocks, st); break;
-    case F32_16: e = launch_f32<16>(a, blocks, st); break;
+    case F32_64: e = launch_f32(a, blocks, st); break;
+    case F32_8:
+      cache_attn_f32_few_kernel<8, 4><<<blocks, 256, 0, st>>>(a);
+      e = cudaGetLastError();
+      break;
+    case F32_4:
+      cache_attn_f32_few_kernel<4, 8><<<blocks, 256, 0, st>>>(a);
+      e = cudaGetLastError();
+      break;
     default: return cudaErrorInvalidValue;
   }
   if (e != cudaSuccess || a.n_split == 1) return e;

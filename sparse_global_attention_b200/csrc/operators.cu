@@ -297,7 +297,7 @@ static int check_attention_sizes(const gsa_kv_cache* c, int64_t n_tokens, int q_
   // rows of a sequence and key head, and blocks of the grid, are counted in 32 bits
   const int64_t rows = static_cast<int64_t>(max_new) * (q_heads / c->kv_heads);
   if (rows >= (1LL << 30) || n_tokens * q_heads >= (1LL << 40) ||
-      static_cast<int64_t>(c->batch) * c->kv_heads * ((rows + 15) / 16) >= (1LL << 24))
+      static_cast<int64_t>(c->batch) * c->kv_heads * ((rows + 7) / 8) >= (1LL << 24))
     return GSA_ERR_UNSUPPORTED;
   return GSA_OK;
 }
