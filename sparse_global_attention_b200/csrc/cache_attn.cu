@@ -1176,10 +1176,10 @@ CacheAttnPlan plan_cache_attn(bool fp32, int batch, int kv_heads, int q_heads, l
   };
   static const Cost costs[] = {{256, 128, 148, 16, 1.4, 1.4, 4.0},       // ROW_TILES
                                {128, 128, 148, 2, 0.75, 0.75, 5.0},      // ONE_TILE
-                               {32, 128, 296, 2, 0.55, 1.5, 4.0},        // QUARTERS
-                               {64, 64, 296, 2, 2.2, 4.2, 6.0},          // F32_64
-                               {8, 64, 296, 2, 0.5, 1.5, 3.0},           // F32_8
-                               {4, 64, 296, 2, 0.4, 1.5, 3.0}};          // F32_4
+                               {32, 128, 296, 2, 0.75, 1.45, 4.0},       // QUARTERS
+                               {64, 64, 296, 1, 5.8, 6.2, 4.0},          // F32_64
+                               {8, 64, 296, 2, 2.0, 2.2, 3.0},           // F32_8
+                               {4, 64, 296, 2, 1.3, 1.5, 3.0}};          // F32_4
   p.kind = fp32 ? (rows <= 4 ? F32_4 : rows <= 24 ? F32_8 : F32_64) : (rows <= 32 ? QUARTERS : rows <= 128 ? ONE_TILE : ROW_TILES);
   const Cost& c = costs[p.kind];
   p.row_tiles = static_cast<int>((rows + c.tile - 1) / c.tile);
@@ -1202,7 +1202,8 @@ CacheAttnPlan plan_cache_attn(bool fp32, int batch, int kv_heads, int q_heads, l
     blocks *= kv_heads;
     const double mean = batch > 1 ? 0.6 : 1.0;
     double best = 1e30;
-    for (long long n = 1; n <= most_splits; ++n) {
+    // (more than a round and a half of blocks: their order evens them out, and parts only cost)
+    for (long long n = 1; n <= most_splits && (n == 1 || blocks < 1.5 * c.slots); ++n) {
       const double chunk = ceil(static_cast<double>(ktiles) / n);
       const double run = blocks * (mean * n + (n > 1 ? 0.5 * (1.0 - mean) : 1.0 - mean));       // blocks with keys
       const double r = run / c.slots;
