@@ -804,6 +804,7 @@ __global__ void __launch_bounds__(256, 2) cache_attn_f32_kernel(const __grid_con
       }
     }
     const int kb = (blk.t_begin + j) * FK;
+    float scale[R];
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       float mx = -INFINITY;
@@ -829,10 +830,15 @@ __global__ void __launch_bounds__(256, 2) cache_attn_f32_kernel(const __grid_con
 #pragma unroll
       for (int w = 1; w < 16; w <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
       l[i] = fmaf(l[i], alpha, sum);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[i][e] *= alpha;
+      scale[i] = alpha;
     }
     __syncwarp();                      // a row's P is written and read by one half-warp
+    // a tile's sums on their own, then into O: a long cache's are not one chain of additions
+    float w[R][4];
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[i][e] = 0.f;
 #pragma unroll 2
     for (int c = 0; c < FK; c += 4) {
       float4 vv[4];
@@ -844,13 +850,17 @@ __global__ void __launch_bounds__(256, 2) cache_attn_f32_kernel(const __grid_con
         const float pe[4] = {p.x, p.y, p.z, p.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          o[i][0] = fmaf(pe[e], vv[e].x, o[i][0]);
-          o[i][1] = fmaf(pe[e], vv[e].y, o[i][1]);
-          o[i][2] = fmaf(pe[e], vv[e].z, o[i][2]);
-          o[i][3] = fmaf(pe[e], vv[e].w, o[i][3]);
+          w[i][0] = fmaf(pe[e], vv[e].x, w[i][0]);
+          w[i][1] = fmaf(pe[e], vv[e].y, w[i][1]);
+          w[i][2] = fmaf(pe[e], vv[e].z, w[i][2]);
+          w[i][3] = fmaf(pe[e], vv[e].w, w[i][3]);
         }
       }
     }
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[i][e] = fmaf(o[i][e], scale[i], w[i][e]);
     __syncthreads();                   // the buffer is refilled in the next step
   }
 #pragma unroll
