@@ -406,7 +406,7 @@ GSA_API int gsa_cache_append(const gsa_kv_cache *cache, const gsa_norm_rope *op,
  *               from cu_tokens[batch] on are left as they are in out
  *   lengths   : int32 [batch], the cached tokens of each sequence
  *   max_new   : at least the most new tokens of a sequence (one that has more is
- *               left out and recorded)
+ *               left out and recorded); max_new * q heads / kv_heads up to 65535 * 64
  *   max_len   : about the longest of `lengths`; it only sets how the work is split
  *   softmax_scale : 0 for 1 / 8
  *   lse       : optional float32 [q heads][n_tokens], log-sum-exp of the scaled scores

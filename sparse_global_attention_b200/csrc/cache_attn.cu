@@ -207,13 +207,12 @@ struct Block {
 template <int TROWS, int TKEYS>
 __device__ __forceinline__ Block block_of(const CacheAttnArgs& a) {
   Block k;
-  unsigned x = blockIdx.x;
-  k.split = x % a.n_split;
-  x /= a.n_split;
-  k.h = x % a.c.heads;
-  x /= a.c.heads;
-  k.b = x % a.c.batch;
-  int tile = static_cast<int>(x / a.c.batch);
+  // key heads fastest, then sequences, tiles and splits: later splits are those that shorter
+  // sequences do not have
+  k.b = blockIdx.x / a.c.heads;
+  k.h = blockIdx.x - k.b * a.c.heads;
+  k.split = blockIdx.z;
+  int tile = blockIdx.y;
   k.seq = sequence_of(a, k.b);
   const long long room = static_cast<long long>(a.c.max_pages) << a.c.page_shift;
   k.len = static_cast<int>(min(static_cast<long long>(k.seq.len), room));
@@ -1138,7 +1137,7 @@ cudaError_t allow_smem(F* kernel, int bytes, std::atomic<unsigned long long>& do
 }
 
 template <int KIND>
-cudaError_t launch_tc(const CacheAttnArgs& a, unsigned blocks, cudaStream_t st) {
+cudaError_t launch_tc(const CacheAttnArgs& a, dim3 blocks, cudaStream_t st) {
   using L = Lay<KIND>;
   static std::atomic<unsigned long long> done{0};
   cudaError_t e = allow_smem(cache_attn_kernel<KIND>, L::BYTES, done);
@@ -1163,7 +1162,7 @@ cudaError_t launch_join(void (*kernel)(CacheAttnArgs), const CacheAttnArgs& a, l
   return cudaLaunchKernelEx(&c, kernel, a);
 }
 
-cudaError_t launch_f32(const CacheAttnArgs& a, unsigned blocks, cudaStream_t st) {
+cudaError_t launch_f32(const CacheAttnArgs& a, dim3 blocks, cudaStream_t st) {
   static std::atomic<unsigned long long> done{0};
   cudaError_t e = allow_smem(cache_attn_f32_kernel, FLay::BYTES, done);
   if (e != cudaSuccess) return e;
@@ -1210,14 +1209,14 @@ CacheAttnPlan plan_cache_attn(bool fp32, int batch, int kv_heads, int q_heads, l
     else
       blocks *= batch;
     blocks *= kv_heads;
-    const double mean = batch > 1 ? 0.6 : 1.0;
+    const double mean = batch > 1 ? 0.7 : 1.0;
     double best = 1e30;
     // (more than a round and a half of blocks: their order evens them out, and parts only cost)
     for (long long n = 1; n <= most_splits && (n == 1 || blocks < 1.5 * c.slots); ++n) {
       const double chunk = ceil(static_cast<double>(ktiles) / n);
       const double run = blocks * (mean * n + (n > 1 ? 0.5 * (1.0 - mean) : 1.0 - mean));       // blocks with keys
       const double r = run / c.slots;
-      const double rounds = r <= 1.0 ? 1.0 : batch > 1 ? r + 0.5 : ceil(r);
+      const double rounds = r <= 1.0 ? 1.0 : batch > 1 ? r + 0.6 : ceil(r);
       const double tile_us = c.alone + (c.busy - c.alone) * (r < 1.0 ? r : 1.0);
       // joining: a launch, and the parts written and read once
       const double join = n > 1 ? 3.0 + n * n_tokens * q_heads * 1.2e-4 : 0.0;
@@ -1235,7 +1234,7 @@ CacheAttnPlan plan_cache_attn(bool fp32, int batch, int kv_heads, int q_heads, l
 }
 
 cudaError_t launch_cache_attn(const CacheAttnArgs& a, bool fp32, int kind, cudaStream_t st) {
-  const unsigned blocks = static_cast<unsigned>(a.c.batch) * a.c.heads * a.row_tiles * a.n_split;
+  const dim3 blocks(static_cast<unsigned>(a.c.batch) * a.c.heads, a.row_tiles, a.n_split);
   cudaError_t e;
   switch (kind) {
     case ROW_TILES: e = launch_tc<ROW_TILES>(a, blocks, st); break;

@@ -294,10 +294,10 @@ static int check_attention_sizes(const gsa_kv_cache* c, int64_t n_tokens, int q_
   GSA_TRY(check_cache(c));
   if (!count_ok(1, n_tokens) || max_new < 0 || max_len < 0 || q_heads < 1 || q_heads > 65535) return GSA_ERR_INVALID_ARG;
   if (q_heads % c->kv_heads) return GSA_ERR_SHAPE;
-  // rows of a sequence and key head, and blocks of the grid, are counted in 32 bits
+  // sequences and key heads, and the tiles of one (at least 64 rows), are dimensions of the grid
   const int64_t rows = static_cast<int64_t>(max_new) * (q_heads / c->kv_heads);
-  if (rows >= (1LL << 30) || n_tokens * q_heads >= (1LL << 40) ||
-      static_cast<int64_t>(c->batch) * c->kv_heads * ((rows + 7) / 8) >= (1LL << 24))
+  if (rows > 65535ll * 64 || n_tokens * q_heads >= (1LL << 40) ||
+      static_cast<int64_t>(c->batch) * c->kv_heads >= (1LL << 31))
     return GSA_ERR_UNSUPPORTED;
   return GSA_OK;
 }
