@@ -364,6 +364,7 @@ __global__ void __launch_bounds__(NTHR, 2) norm_rope_bwd_kernel(const __grid_con
   const int lane = threadIdx.x & 31, r = lane >> 3;
   const int c0 = Chan<AXES>::first(lane & 7);
   constexpr int APART = Chan<AXES>::APART;
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   int blk = blockIdx.x, role = 0;
   while (blk >= a.blocks[role]) blk -= a.blocks[role++];
   const Rows gin = a.dout[role], gout = a.din[role];
@@ -504,13 +505,21 @@ __global__ void __launch_bounds__(NTHR, 2) norm_rope_bwd_kernel(const __grid_con
   }
 }
 
-// one block per tensor: column c of the blocks' rows [blocks][128], eight interleaved chains
+// one block per tensor: column c of the blocks' rows [blocks][128], eight interleaved chains of
+// eight loads at a time; launched while the blocks still run (programmatic dependent launch)
 __global__ void __launch_bounds__(1024) norm_rope_sum_kernel(const __grid_constant__ NormRopeBwdArgs a) {
   __shared__ float sums[8][128];
-  const int col = threadIdx.x & 127, grp = threadIdx.x >> 7, role = blockIdx.x;
+  const int col = threadIdx.x & 127, grp = threadIdx.x >> 7, role = blockIdx.x, n = a.blocks[role];
+  const float* p = a.part + static_cast<long long>(role) * NORM_BWD_BLOCKS * 128 + col;
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
   float v = 0.f;
-#pragma unroll 4
-  for (int i = grp; i < a.blocks[role]; i += 8) v += a.part[(static_cast<long long>(role) * NORM_BWD_BLOCKS + i) * 128 + col];
+  for (int i = grp; i < n; i += 64) {
+    float x[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x[k] = i + 8 * k < n ? p[(i + 8 * k) * 128] : 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v += x[k];
+  }
   sums[grp][col] = v;
   __syncthreads();
   if (grp == 0) {
@@ -578,7 +587,20 @@ cudaError_t launch_bwd(NormRopeBwdArgs a, cudaStream_t st) {
   }
   if (total > 0) norm_rope_bwd_kernel<T, G, NORM, AXES><<<total, NTHR, 0, st>>>(a);
   // a tensor that is left out has no sums to write (its pointers are null)
-  if (a.part && NORM != NORM_NONE) norm_rope_sum_kernel<<<2, 1024, 0, st>>>(a);
+  if (a.part && NORM != NORM_NONE) {
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute early;
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t c = {};
+    c.gridDim = dim3(2);
+    c.blockDim = dim3(1024);
+    c.stream = st;
+    c.attrs = &early;
+    c.numAttrs = total > 0 ? 1 : 0;      // behind this call's blocks only
+    return cudaLaunchKernelEx(&c, norm_rope_sum_kernel, a);
+  }
   return cudaGetLastError();
 }
 
