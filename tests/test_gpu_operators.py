@@ -719,3 +719,50 @@ def test_a_timeout_of_the_other_calls_does_not_show_here():
     gsa.gsa_debug_expire_wait(None, 1000, torch.cuda.current_stream().cuda_stream)
     clean()
     assert gsa.gsa_special_attention_noalloc_status(torch.cuda.current_stream().cuda_stream) == 6
+
+
+# ---- offsets beyond 32 bits ----------------------------------------------------------------------
+def test_pages_beyond_32_bit_offsets():
+    """A pool of more than 2^31 elements: the sequence's pages lie at its end."""
+    page, hk, pages = 256, 16, 8400
+    assert pages * hk * page * 64 > 2 ** 31
+    cache = gsa.KVCache(pages, page, hk)
+    g = torch.Generator(device="cuda").manual_seed(0)
+    rand = lambda t, h: torch.randn(t, h, 64, generator=g, device="cuda").bfloat16()
+    table = torch.tensor([[pages - 1, 3, pages - 2]], dtype=torch.int32, device="cuda")
+    n = 600
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    k, v = rand(n, hk), rand(n, hk)
+    cache.append(k, v, table, i32([0]), i32([0, n]))
+    assert torch.equal(cache.k_pages[pages - 1], k[:256].transpose(0, 1))
+    assert torch.equal(cache.v_pages[pages - 2, :, :88], v[512:].transpose(0, 1))
+    for new, group in ((1, 1), (70, 1), (200, 1)):
+        q = rand(new, hk * group)
+        out = cache.attention(q, table, i32([n]), i32([0, new]), new)
+        seen = np.arange(n)[None] <= np.arange(n - new, n)[:, None]
+        for h in (0, hk - 1):
+            kd, vd, qd = f64(k[:, h]), f64(v[:, h]), f64(q[:, h])
+            s = np.where(seen, qd @ kd.T / 8, -np.inf)
+            p = np.exp(s - s.max(-1, keepdims=True))
+            p /= p.sum(-1, keepdims=True)
+            a = np.abs(qd).sum(-1).max() * np.abs(kd).max() / 8
+            assert_within("out", f64(out[:, h]), p @ vd, (128 * (1 + a) * U + n * U + 2.0 ** -8) * (p @ np.abs(vd)) + 2.0 ** -8 * np.abs(p @ vd))
+    clean()
+
+
+def test_rows_beyond_32_bit_offsets():
+    tokens, heads = (1 << 21) + 5, 16
+    assert tokens * heads * 64 > 2 ** 31
+    x = torch.empty(1, tokens, heads, 64, dtype=torch.bfloat16, device="cuda")
+    x[:, -7:] = torch.randn(1, 7, heads, 64, device="cuda")
+    x[:, :3] = torch.randn(1, 3, heads, 64, device="cuda")
+    w = torch.randn(64, device="cuda").bfloat16()
+    pos = torch.arange(tokens, dtype=torch.int32, device="cuda").unsqueeze(-1)
+    for head_major in (False, True):
+        y = gsa.qk_norm_rope(x, norm="rms", q_weight=w, positions=pos, rope_base=10000.0, head_major=head_major)[0]
+        y = y.permute(1, 2, 0, 3) if head_major else y
+        for part in (slice(0, 3), slice(-7, None)):
+            check_norm_rope({"q": x[:, part]}, {"q_weight": w}, pos[None, part], "rms", 1, 10000.0, {"q": y[:, part]},
+                            torch.bfloat16, 1e-5)
+        del y
+    clean()
