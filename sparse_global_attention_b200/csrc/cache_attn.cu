@@ -1184,8 +1184,8 @@ CacheAttnPlan plan_cache_attn(bool fp32, int batch, int kv_heads, int q_heads, l
     double alone, busy, start;
   };
   static const Cost costs[] = {{256, 128, 148, 16, 1.4, 1.4, 4.0},       // ROW_TILES
-                               {128, 128, 148, 2, 0.75, 0.75, 5.0},      // ONE_TILE
-                               {32, 128, 296, 2, 0.75, 1.45, 4.0},       // QUARTERS
+                               {128, 128, 148, 2, 0.36, 0.75, 5.0},      // ONE_TILE
+                               {32, 128, 296, 2, 0.55, 1.45, 4.0},       // QUARTERS
                                {64, 64, 296, 1, 5.8, 6.2, 4.0},          // F32_64
                                {8, 64, 296, 2, 2.0, 2.2, 3.0},           // F32_8
                                {4, 64, 296, 2, 1.3, 1.5, 3.0}};          // F32_4
@@ -1209,17 +1209,17 @@ CacheAttnPlan plan_cache_attn(bool fp32, int batch, int kv_heads, int q_heads, l
     else
       blocks *= batch;
     blocks *= kv_heads;
-    const double mean = batch > 1 ? 0.7 : 1.0;
+    const double mean = batch > 1 ? 0.85 : 1.0;
     double best = 1e30;
     // (more than a round and a half of blocks: their order evens them out, and parts only cost)
     for (long long n = 1; n <= most_splits && (n == 1 || blocks < 1.5 * c.slots); ++n) {
       const double chunk = ceil(static_cast<double>(ktiles) / n);
       const double run = blocks * (mean * n + (n > 1 ? 0.5 * (1.0 - mean) : 1.0 - mean));       // blocks with keys
       const double r = run / c.slots;
-      const double rounds = r <= 1.0 ? 1.0 : batch > 1 ? r + 0.6 : ceil(r);
+      const double rounds = r <= 1.0 ? 1.0 : batch > 1 ? fmin(r + 0.6, 2.0 * r - 1.0) : ceil(r);
       const double tile_us = c.alone + (c.busy - c.alone) * (r < 1.0 ? r : 1.0);
       // joining: a launch, and the parts written and read once
-      const double join = n > 1 ? 3.0 + n * n_tokens * q_heads * 1.2e-4 : 0.0;
+      const double join = n > 1 ? 4.4 + n * (0.08 + n_tokens * q_heads * 1e-4) : 0.0;
       const double t = rounds * (chunk * tile_us + 0.5 * c.start) + 0.5 * c.start + join;
       if (t < best * 0.95) {
         best = t;
