@@ -1,23 +1,23 @@
 // Per-head norm of queries and keys with the position rotation in one pass,
 // its gradients, and the same pass writing keys (and values) into a paged cache.
 //
-// A row is the 64 channels of one (token, head).  Eight lanes hold a row, so a warp
-// works on four heads of a token at a time (a quad) and every sum over a row is three
-// shuffles.  A lane holds four channels and the four that the rotation pairs them with
+// A row is the 64 channels of one (token, head).  Eight lanes hold a row and every sum over a
+// row is three shuffles.  A warp works on four heads of a token at a time (a quad) or, in large
+// calls, on four tokens.  A lane holds four channels and the four that the rotation pairs them with
 // (i and i + 32, or i and i + 16 inside a half), so the rotation needs no exchange, and
 // the arithmetic runs on pairs of channels (packed fp32: the passes are near the issue
 // limit, 1,800 instructions a token of 16 heads in the one-channel form with exchanged
 // partners took 123 us where the bytes take 78).  Mean and variance come from the row in
 // registers (the variance from the centred values), everything is fp32 with one rounding
-// at the store.  The 32 angles of a token are computed once, one per lane, and serve all
+// at the store.  The 32 angles of a token are computed once and serve all
 // its heads.  An angle is a part of a turn in 64-bit fixed point (position times turns per
 // position modulo 2^64 is one integer product, off by 2^-34 of a turn at the most), so
 // positions far into a stream lose nothing; its upper half goes to sincospif.
 //
-// Bound by HBM.  Each warp loads all quads of its item before it works on them; a grid of
-// what the SMs hold keeps the tokens in flight together, so that the rows of each head are
-// written side by side (128 frames of 1296 tokens and 16 heads, 2.04 GB: 393 us, 5.2 TB/s;
-// a block for every eight tokens instead: 503 us).
+// Bound by HBM.  Each warp loads the rows of four heads a lane before it works on them; a grid
+// of what the SMs hold keeps the tokens in flight together, so that the rows of each head are
+// written side by side (128 frames of 1296 tokens and 16 heads, 2.04 GB: 363 us, 5.6 TB/s; in
+// quads 396 us, in quads with a block for every eight tokens 503 us).
 #include "gsa_common.cuh"
 #include "operators.h"
 
@@ -140,6 +140,19 @@ struct Turn {
 #pragma unroll
     for (int k = 0; k < 2; ++k) ns[k] = make_float2(-s[k].x, -s[k].y);
   }
+  // the lane's own four pairs, f their turns per unit: every group of eight lanes has a token of its own
+  __device__ __forceinline__ void set_own(const unsigned long long* f, int p0, int p1, int lane) {
+    const long long p = AXES == 2 && (lane & 4) ? p1 : p0;
+    float* cp = reinterpret_cast<float*>(c);
+    float* sp = reinterpret_cast<float*>(s);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const long long turn = static_cast<long long>(static_cast<unsigned long long>(p) * f[e]);
+      sincospif(static_cast<float>(static_cast<int>(turn >> 32)) * 4.656612873077393e-10f, &sp[e], &cp[e]);
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) ns[k] = make_float2(-s[k].x, -s[k].y);
+  }
   // rotate by the angle (DIR = 1) or back (DIR = -1)
   template <int DIR>
   __device__ __forceinline__ void apply(Lane8& y) const {
@@ -154,6 +167,7 @@ struct Turn {
 template <>
 struct Turn<0> {
   __device__ __forceinline__ void set(unsigned long long, int, int, int) {}
+  __device__ __forceinline__ void set_own(const unsigned long long*, int, int, int) {}
   template <int DIR>
   __device__ __forceinline__ void apply(Lane8&) const {}
 };
@@ -241,23 +255,37 @@ __device__ __forceinline__ int find_sequence(const int* cu, int n, long long t, 
   return lo;
 }
 
-// element of new token t in a pool (head 0), -1 if it has no page; and its place in its sequence
-__device__ __forceinline__ long long paged_row(const NormRopeArgs& a, long long t, int lane, int& place) {
+// element of new token t of sequence b in a pool (head 0), -1 if it has no page; and its place in its
+// sequence.  `tell`: the thread that records what is wrong.
+__device__ __forceinline__ long long place_row(const NormRopeArgs& a, int b, long long t, bool tell, int& place) {
   const PagedCache& c = a.c;
-  if (a.cu[0] > t) return -1;
-  const int b = find_sequence(a.cu, c.batch, t, lane);
-  if (b >= c.batch) return -1;                             // behind the last sequence
   const int first = a.cu[b], start = a.start[b];
   const long long at = static_cast<long long>(start) + (t - first);
   int page = -1;
   if (first <= t && a.cu[b + 1] > t && start >= 0 && (at >> c.page_shift) < c.max_pages)
     page = c.table[b * c.table_stride + (at >> c.page_shift)];
   if (page < 0 || page >= c.num_pages) {
-    if (lane == 0) set_error(a.err, ERR_BOUNDS);
+    if (tell) set_error(a.err, ERR_BOUNDS);
     return -1;
   }
   place = static_cast<int>(at);
   return ((static_cast<long long>(page) * c.heads << c.page_shift) + (at & ((1 << c.page_shift) - 1))) * D;
+}
+// a token of the whole warp
+__device__ __forceinline__ long long paged_row(const NormRopeArgs& a, long long t, int lane, int& place) {
+  if (a.cu[0] > t) return -1;
+  const int b = find_sequence(a.cu, a.c.batch, t, lane);
+  return b >= a.c.batch ? -1 : place_row(a, b, t, lane == 0, place);      // -1: behind the last sequence
+}
+// a token of this lane's group
+__device__ __forceinline__ long long paged_row_of(const NormRopeArgs& a, long long t, bool tell, int& place) {
+  if (a.cu[0] > t || a.cu[a.c.batch] <= t) return -1;
+  int lo = 0, hi = a.c.batch;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (a.cu[mid] <= t) lo = mid; else hi = mid;
+  }
+  return place_row(a, lo, t, tell, place);
 }
 
 // An item is up to U quads of one token: `left` heads from `head` on.
@@ -348,6 +376,92 @@ __global__ void __launch_bounds__(NTHR, 3) norm_rope_kernel(const __grid_constan
           raw[u].a.store(po + 4 * u * out.sh);
           raw[u].b.store(po + 4 * u * out.sh + APART);
         }
+      }
+    }
+  }
+}
+
+// Large calls: each group of eight lanes takes a token of its own and goes through its heads four at a
+// time, with its own angles (four a lane).  No lane is left without a row whatever the heads are, and
+// the angles cost a token, not a head; but a warp holds four tokens and has to go through all their
+// heads, which makes small calls longer.  launch_fwd has the rule between the two and its figures.
+template <typename T, int NORM, int AXES, bool PAGED>
+__global__ void __launch_bounds__(NTHR, 3) norm_rope_group_kernel(const __grid_constant__ NormRopeArgs a) {
+  const int lane = threadIdx.x & 31, r = lane >> 3;
+  const int c0 = Chan<AXES>::first(lane & 7);
+  constexpr int APART = Chan<AXES>::APART;
+  const long long tokens = a.n_outer * a.n_tokens, items = (tokens + 3) >> 2;
+  const long long step = static_cast<long long>(gridDim.x) * WARPS;
+  long long item = static_cast<long long>(blockIdx.x) * WARPS + (threadIdx.x >> 5);
+  unsigned long long f[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) f[e] = AXES == 0 ? 0 : a.rope.f[(4 * (lane & 7) + e) & (AXES == 2 ? 15 : 31)];
+  long long end = 0;                                       // first item behind the tensor
+#pragma unroll 1
+  for (int role = PAGED ? 1 : 0; role < 3; ++role) {
+    const Rows in = a.in[role], out = a.out[role];
+    if (in.heads == 0) continue;
+    const long long begin = end;
+    end += items;
+    if (item >= end) continue;                             // this warp has none of it
+    Affine<T, NORM> af;
+    if (role < 2) af.load(a.w[role], a.b[role], c0, APART);
+    const T* src = static_cast<const T*>(in.p) + c0;
+    T* dst = static_cast<T*>(out.p) + c0;
+#pragma unroll 1
+    for (; item < end; item += step) {
+      const long long g = 4 * (item - begin) + r;
+      const bool real = g < tokens;
+      long long o, t;
+      split_token(real ? g : 0, a.n_tokens, o, t);
+      const T* pi = src + o * in.so + t * in.st;
+      Raw8<T> raw[4];
+      const auto fetch = [&](int h0) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          raw[u].a.zero();
+          raw[u].b.zero();
+          if (h0 + u < in.heads && real) {
+            raw[u].a.load(pi + (h0 + u) * in.sh);
+            raw[u].b.load(pi + (h0 + u) * in.sh + APART);
+          }
+        }
+      };
+      fetch(0);
+      int p0 = 0, p1 = 0;
+      long long at = 0;
+      if constexpr (PAGED) at = real ? paged_row_of(a, t, (lane & 7) == 0, p0) : -1;
+      else at = o * out.so + t * out.st;
+      Turn<AXES> turn;
+      if (AXES > 0 && role < 2) {
+        if (a.pos) {
+          const int* q = a.pos + o * a.pos_so + t * AXES;
+          p0 = q[0];
+          if constexpr (AXES == 2) p1 = q[1];
+        }
+        turn.set_own(f, p0, p1, lane);
+      }
+#pragma unroll 1
+      for (int h0 = 0;;) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          if (h0 + u >= in.heads) break;                   // the whole warp
+          if (role < 2) {
+            Lane8 x;
+            raw[u].get(x);
+            norm_row<NORM>(x, a.eps);
+            af.apply(x);
+            turn.template apply<1>(x);
+            raw[u].put(x);
+          }
+          if (real && (!PAGED || at >= 0)) {
+            T* po = dst + at + (h0 + u) * out.sh;
+            raw[u].a.store(po);
+            raw[u].b.store(po + APART);
+          }
+        }
+        if ((h0 += 4) >= in.heads) break;
+        fetch(h0);
       }
     }
   }
@@ -553,12 +667,32 @@ int blocks_for(long long items, int most) {
   }                                                                         \
   return cudaErrorInvalidValue;
 
+// Which of the two kernels: small calls last as long as their longest warp, which in groups goes
+// through all heads one after the other and in quads has items / warps of them; measured even at
+// about an eighth of the heads (16 heads: 1369 tokens, three tensors, 6.3 us in quads, 8.0 in groups;
+// 3001 tokens, two tensors, 8.8 and 9.0; 8 heads 7.8 and 6.5, 2 heads 7.0 and 4.8, but 48 tokens of
+// them 3.4 and 3.7).  Above that groups in 16 bits:
+// 60,000 tokens of queries and keys, us in quads and in groups, 4 heads 54 and 26, 7 heads 67 and 43,
+// 16 heads 92 and 90, 24 heads 170 and 130; three tensors of 16 heads with two axes, 165,888 tokens,
+// 396 and 363.  In 32 bits a quad's lanes hold twice the bytes and the memory is the bound once they
+// are full, so groups only where a quarter of the lanes or more would have no row: 4 heads 52 and 44,
+// 10 heads 131 and 107, but 8 heads 75 and 83, 16 heads 153 and 166, 32 heads 300 and 332.
 template <typename T, int NORM, int AXES, bool PAGED>
 cudaError_t launch_fwd(const NormRopeArgs& a, cudaStream_t st) {
-  constexpr int PER = 4 * (sizeof(T) == 2 ? 4 : 2);        // heads of an item
-  long long items = 0;
-  for (int i = PAGED ? 1 : 0; i < 3; ++i) items += a.n_outer * a.n_tokens * ((a.in[i].heads + PER - 1) / PER);
-  norm_rope_kernel<T, NORM, AXES, PAGED><<<blocks_for(items, FWD_BLOCKS), NTHR, 0, st>>>(a);
+  constexpr int PER = 4 * (sizeof(T) == 2 ? 4 : 2);        // heads of an item of quads
+  const long long tokens = a.n_outer * a.n_tokens;
+  long long items = 0, tensors = 0, heads = 0, most = 0;
+  for (int i = PAGED ? 1 : 0; i < 3; ++i) {
+    heads += tokens * a.in[i].heads;
+    items += tokens * ((a.in[i].heads + PER - 1) / PER);
+    tensors += a.in[i].heads > 0;
+    if (a.in[i].heads > most) most = a.in[i].heads;
+  }
+  if (8 * items > FWD_BLOCKS * WARPS * most && (sizeof(T) == 2 || 4 * heads <= 3 * PER * items))
+    norm_rope_group_kernel<T, NORM, AXES, PAGED>
+        <<<blocks_for(tensors * ((tokens + 3) / 4), FWD_BLOCKS), NTHR, 0, st>>>(a);
+  else
+    norm_rope_kernel<T, NORM, AXES, PAGED><<<blocks_for(items, FWD_BLOCKS), NTHR, 0, st>>>(a);
   return cudaGetLastError();
 }
 

@@ -102,6 +102,29 @@ def test_norm_rope(outer, tokens, hq, hk, dtype, norm, axes):
     clean()
 
 
+@pytest.mark.parametrize("norm,axes", [("none", 2), ("layer", 2), ("rms", 1), ("layer", 0), ("rms", 2), ("layer", 1)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("hq,hk", [(1, 1), (6, 2), (21, 7)])
+def test_norm_rope_of_many_tokens(hq, hk, dtype, norm, axes):
+    """More tokens than warps: every group of lanes has a token of its own; a count that no four divide."""
+    test_norm_rope(3, 1201, hq, hk, dtype, norm, axes)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_norm_rope_of_many_tokens_in_place_and_with_strides(dtype):
+    g = torch.Generator(device="cuda").manual_seed(9)
+    dt, n = TYPES[dtype], 2501
+    y = torch.randn(2, n, 7, 64, generator=g, device="cuda").to(dt)
+    w = {a: (1 + 0.2 * torch.randn(64, generator=g, device="cuda")).to(dt) for a in ("q_weight", "k_weight")}
+    pos = torch.randint(0, 40, (n, 2), generator=g, device="cuda", dtype=torch.int32)
+    x = y.clone()
+    gsa.qk_norm_rope(y[:, :, :5], y[:, :, 5:6], norm="rms", positions=pos, out=(y[:, :, :5], y[:, :, 5:6], None), **w)
+    check_norm_rope({"q": x[:, :, :5], "k": x[:, :, 5:6]}, w, pos[None].expand(2, n, 2), "rms", 2, 100.0,
+                    {"q": y[:, :, :5], "k": y[:, :, 5:6]}, dt, 1e-5)
+    assert torch.equal(y[:, :, 6], x[:, :, 6])
+    clean()
+
+
 @pytest.mark.parametrize("axes", [1, 2])
 def test_positions_at_the_ends_of_their_range(axes):
     g = torch.Generator(device="cuda").manual_seed(5)
@@ -326,6 +349,25 @@ def test_append(new, old, page, hk, dtype, norm, axes):
     assert np.array_equal(np.isnan(f64(s.cache.k_pages)), untouched)
     want, _ = oo.cache_append(f64(before[1]), f64(v[:tokens]), table, old, s.cu_list)
     assert np.array_equal(f64(s.cache.v_pages), want, equal_nan=True)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("norm,axes", [("none", 0), ("rms", 1), ("layer", 2)])
+@pytest.mark.parametrize("new,old,page,hk", [([0, 900, 0, 1100, 1, 0], [4, 100, 0, 0, 63, 9], 16, 3), ([2, 1902], [0, 30], 128, 8)])
+def test_append_of_many_tokens(new, old, page, hk, dtype, norm, axes):
+    test_append(new, old, page, hk, dtype, norm, axes)
+
+
+def test_append_of_many_tokens_leaves_out_what_has_no_page():
+    s = Streams([1000, 1000], [10, 10], 16, 2, torch.bfloat16)
+    s.table[0, 3], s.table[1, 5] = s.cache.num_pages, -1
+    k, v = s.rand(2000, 2), s.rand(2000, 2)
+    before = f64(s.cache.v_pages)
+    s.cache.append(k, v, s.table, s.start, s.cu, norm="none", rope_axes=1)
+    assert gsa.operator_status() == 7
+    clean()
+    want, left = oo.cache_append(before, f64(v), s.table.cpu().numpy(), [10] * 2, s.cu_list)
+    assert len(left) == 32 and np.array_equal(f64(s.cache.v_pages), want, equal_nan=True)
 
 
 def test_append_leaves_out_what_has_no_page():
