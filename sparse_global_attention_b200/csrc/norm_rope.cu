@@ -173,6 +173,12 @@ struct Turn<0> {
 };
 
 // turns per unit of position of this lane's channel pair, in 2^-64
+// of the lane's own four pairs
+template <int AXES>
+__device__ __forceinline__ void own_freq(const RopeTable& t, int lane, unsigned long long (&f)[4]) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) f[e] = AXES == 0 ? 0 : t.f[(4 * (lane & 7) + e) & (AXES == 2 ? 15 : 31)];
+}
 template <int AXES>
 __device__ __forceinline__ unsigned long long lane_freq(const RopeTable& r, int lane) {
   if constexpr (AXES == 0) return 0;
@@ -394,8 +400,7 @@ __global__ void __launch_bounds__(NTHR, 3) norm_rope_group_kernel(const __grid_c
   const long long step = static_cast<long long>(gridDim.x) * WARPS;
   long long item = static_cast<long long>(blockIdx.x) * WARPS + (threadIdx.x >> 5);
   unsigned long long f[4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) f[e] = AXES == 0 ? 0 : a.rope.f[(4 * (lane & 7) + e) & (AXES == 2 ? 15 : 31)];
+  own_freq<AXES>(a.rope, lane, f);
   long long end = 0;                                       // first item behind the tensor
 #pragma unroll 1
   for (int role = PAGED ? 1 : 0; role < 3; ++role) {
@@ -471,7 +476,9 @@ __global__ void __launch_bounds__(NTHR, 3) norm_rope_group_kernel(const __grid_c
 // db += g, dw += g h, u = g w, dx = r (u - mean(u) - h mean(u h)) (RMS: without
 // mean(u)).  Blocks are dealt to the tensors by their bytes; a block's weight sums
 // go to its own row of `part`, and a second kernel adds those in a fixed order.
-template <typename T, typename G, int NORM, int AXES>
+// GROUPS: a token per group of lanes and two of its heads at a time, else two quads of a token; the
+// next two rows of a lane are on their way while it works on these.
+template <typename T, typename G, int NORM, int AXES, bool GROUPS>
 __global__ void __launch_bounds__(NTHR, 2) norm_rope_bwd_kernel(const __grid_constant__ NormRopeBwdArgs a) {
   constexpr int U = 2;
   constexpr bool NORMED = NORM != NORM_NONE;
@@ -483,17 +490,21 @@ __global__ void __launch_bounds__(NTHR, 2) norm_rope_bwd_kernel(const __grid_con
   while (blk >= a.blocks[role]) blk -= a.blocks[role++];
   const Rows gin = a.dout[role], gout = a.din[role];
   const Rows xin = a.in[role < 2 ? role : 0];
-  const int batches = (gin.heads + 4 * U - 1) / (4 * U);
-  const long long items = a.n_outer * a.n_tokens * batches, step = static_cast<long long>(a.blocks[role]) * WARPS;
-  const unsigned long long f = lane_freq<AXES>(a.rope, lane);
+  constexpr int NEXT = GROUPS ? 1 : 4, OFF = GROUPS ? 0 : 1;      // heads from one row of a lane to its next; of lanes
+  const int batches = (gin.heads + NEXT * U - 1) / (NEXT * U);
+  const long long tokens = a.n_outer * a.n_tokens, step = static_cast<long long>(a.blocks[role]) * WARPS;
+  const long long items = GROUPS ? (tokens + 3) >> 2 : tokens * batches;
+  unsigned long long f[GROUPS ? 4 : 1];
+  if constexpr (GROUPS) own_freq<AXES>(a.rope, lane, f);
+  else f[0] = lane_freq<AXES>(a.rope, lane);
   Affine<T, NORMED ? NORM_RMS : NORM_NONE> af;
   if (role < 2) af.load(a.w[role], nullptr, c0, APART);
   Lane8 dw, db;
 #pragma unroll
   for (int k = 0; k < 4; ++k) dw.v[k] = db.v[k] = both(0.f);
-  const G* pg = static_cast<const G*>(gin.p) + r * gin.sh + c0;
-  const T* px = static_cast<const T*>(xin.p) + r * xin.sh + c0;
-  G* po = static_cast<G*>(gout.p) + r * gout.sh + c0;
+  const G* pg = static_cast<const G*>(gin.p) + OFF * r * gin.sh + c0;
+  const T* px = static_cast<const T*>(xin.p) + OFF * r * xin.sh + c0;
+  G* po = static_cast<G*>(gout.p) + OFF * r * gout.sh + c0;
   const bool with_x = NORMED && role < 2;
 
   Raw8<G> rg[U];
@@ -505,32 +516,44 @@ __global__ void __launch_bounds__(NTHR, 2) norm_rope_bwd_kernel(const __grid_con
   }
   int p0 = 0, p1 = 0;
   Item it;
-  auto load = [&](long long x) {
-    it.at(x, batches, 4 * U, a.n_tokens);
+  bool mine = true;                                        // this lane's token is one
+  long long item = static_cast<long long>(blk) * WARPS + (threadIdx.x >> 5);
+  int batch = 0;                                           // GROUPS: of the item
+  auto load = [&]() {
+    if constexpr (GROUPS) {
+      it.head = batch * U;
+      if (batch == 0) {
+        const long long g = 4 * item + r;
+        mine = g < tokens;
+        split_token(mine ? g : 0, a.n_tokens, it.o, it.t);
+      }
+    } else {
+      it.at(item, batches, 4 * U, a.n_tokens);
+    }
     const G* g = pg + it.o * gin.so + it.t * gin.st + it.head * gin.sh;
     const T* p = px + it.o * xin.so + it.t * xin.st + it.head * xin.sh;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       rg[u].a.zero();
       rg[u].b.zero();
-      if (it.head + 4 * u + r < gin.heads) {
-        rg[u].a.load(g + 4 * u * gin.sh);
-        rg[u].b.load(g + 4 * u * gin.sh + APART);
+      if (mine && it.head + NEXT * u + OFF * r < gin.heads) {
+        rg[u].a.load(g + NEXT * u * gin.sh);
+        rg[u].b.load(g + NEXT * u * gin.sh + APART);
         if (with_x) {
-          rx[u].a.load(p + 4 * u * xin.sh);
-          rx[u].b.load(p + 4 * u * xin.sh + APART);
+          rx[u].a.load(p + NEXT * u * xin.sh);
+          rx[u].b.load(p + NEXT * u * xin.sh + APART);
         }
       }
     }
-    if (AXES > 0 && role < 2) {
+    if (AXES > 0 && role < 2 && batch == 0) {
       const int* q = a.pos + it.o * a.pos_so + it.t * AXES;
       p0 = q[0];
       if constexpr (AXES == 2) p1 = q[1];
     }
   };
-  long long item = static_cast<long long>(blk) * WARPS + (threadIdx.x >> 5);
+  Turn<AXES> turn;
   bool more = item < items;
-  if (more) load(item);
+  if (more) load();
 #pragma unroll 1
   while (more) {
     Raw8<G> ng[U];
@@ -541,17 +564,22 @@ __global__ void __launch_bounds__(NTHR, 2) norm_rope_bwd_kernel(const __grid_con
       nx[u] = rx[u];
     }
     const Item cur = it;
-    const int q0 = p0, q1 = p1;
-    item += step;
+    const bool have = mine;
+    if (role < 2 && batch == 0) {
+      if constexpr (GROUPS) turn.set_own(f, p0, p1, lane);
+      else turn.set(f[0], p0, p1, lane);
+    }
+    if (!GROUPS || ++batch == batches) {
+      batch = 0;
+      item += step;
+    }
     more = item < items;
-    if (more) load(item);
+    if (more) load();
     G* p = po + cur.o * gout.so + cur.t * gout.st + cur.head * gout.sh;
-    Turn<AXES> turn;
-    if (role < 2) turn.set(f, q0, q1, lane);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (cur.head + 4 * u >= gin.heads) break;            // the whole warp
-      const bool real = cur.head + 4 * u + r < gin.heads;
+      if (cur.head + NEXT * u >= gin.heads) break;         // the whole warp
+      const bool real = have && cur.head + NEXT * u + OFF * r < gin.heads;
       if (role < 2) {
         Lane8 d;
         ng[u].get(d);                                      // zeros where there is no head
@@ -583,8 +611,8 @@ __global__ void __launch_bounds__(NTHR, 2) norm_rope_bwd_kernel(const __grid_con
         ng[u].put(d);
       }
       if (real) {
-        ng[u].a.store(p + 4 * u * gout.sh);
-        ng[u].b.store(p + 4 * u * gout.sh + APART);
+        ng[u].a.store(p + NEXT * u * gout.sh);
+        ng[u].b.store(p + NEXT * u * gout.sh + APART);
       }
     }
   }
@@ -702,24 +730,38 @@ cudaError_t launch_norm_rope(const NormRopeArgs& a, bool fp32, int norm, int axe
 #undef GSA_CALL
 }
 
+// Quads or groups as in the forward; measured even at a quarter of the heads (us, queries and keys: 16
+// heads, 3001 tokens 16.1 and 15.7, 8 heads 10.6 and 10.7, 2 heads 9.3 and 6.8; 700 tokens of 4 heads 6.1
+// and 6.1, of 10 heads 8.6 and 9.1).  60,000 tokens in 16 bits: 2 heads 69 and 30, 8 heads 93 and 81, 16
+// heads 188 and 151, 24 heads 277 and 220; three tensors of 16 heads with gradients in 32 bits and two
+// axes, 217 and 197.  In 32 bits: 2 heads 77 and 35, 12 heads 203 and 184, but 16 heads 229 and 247.
 template <typename T, typename G, int NORM, int AXES>
 cudaError_t launch_bwd(NormRopeBwdArgs a, cudaStream_t st) {
-  // blocks by each tensor's bytes, at most what has items
+  const long long tokens = a.n_outer * a.n_tokens;
   double bytes[3], all = 0.0;
+  long long quads = 0, heads = 0, most = 0;
   for (int i = 0; i < 3; ++i) {
     bytes[i] = a.dout[i].heads * (2.0 * sizeof(G) + (i < 2 && NORM != NORM_NONE ? sizeof(T) : 0));
     all += bytes[i];
+    quads += tokens * ((a.dout[i].heads + 7) / 8);
+    heads += tokens * a.dout[i].heads;
+    if (a.dout[i].heads > most) most = a.dout[i].heads;
   }
+  const bool groups = 4 * quads > NORM_BWD_BLOCKS * WARPS * most && (sizeof(T) == 2 || 4 * heads <= 3 * 8 * quads);
+  // blocks by each tensor's bytes, at most what has items
   int total = 0;
   for (int i = 0; i < 3; ++i) {
     a.blocks[i] = 0;
-    const long long items = a.n_outer * a.n_tokens * ((a.dout[i].heads + 7) / 8);
-    if (items == 0) continue;
+    if (tokens == 0 || a.dout[i].heads == 0) continue;
+    const long long items = groups ? (tokens + 3) / 4 : tokens * ((a.dout[i].heads + 7) / 8);
     const int share = static_cast<int>(NORM_BWD_BLOCKS * bytes[i] / all);
     a.blocks[i] = blocks_for(items, share < 1 ? 1 : share);
     total += a.blocks[i];
   }
-  if (total > 0) norm_rope_bwd_kernel<T, G, NORM, AXES><<<total, NTHR, 0, st>>>(a);
+  if (total > 0) {
+    if (groups) norm_rope_bwd_kernel<T, G, NORM, AXES, true><<<total, NTHR, 0, st>>>(a);
+    else norm_rope_bwd_kernel<T, G, NORM, AXES, false><<<total, NTHR, 0, st>>>(a);
+  }
   // a tensor that is left out has no sums to write (its pointers are null)
   if (a.part && NORM != NORM_NONE) {
     const cudaError_t e = cudaGetLastError();

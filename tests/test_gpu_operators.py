@@ -227,6 +227,14 @@ def test_norm_rope_backward(outer, tokens, hq, hk, dtype, gdtype, norm, axes):
     clean()
 
 
+@pytest.mark.parametrize("norm,axes", [("none", 2), ("layer", 2), ("rms", 1), ("layer", 0)])
+@pytest.mark.parametrize("dtype,gdtype", [("bf16", "fp32"), ("bf16", "bf16"), ("fp32", "fp32")])
+@pytest.mark.parametrize("outer,tokens,hq,hk", [(3, 1201, 1, 1), (2, 1802, 6, 2), (1, 3603, 21, 7)])
+def test_norm_rope_backward_of_many_tokens(outer, tokens, hq, hk, dtype, gdtype, norm, axes):
+    """More tokens than warps: every group of lanes has a token of its own; counts that no four divide."""
+    test_norm_rope_backward(outer, tokens, hq, hk, dtype, gdtype, norm, axes)
+
+
 def test_norm_rope_backward_against_differences():
     """The kernel's gradient against central differences of the kernel's forward, fp32, step h = 2^-6: an output is off
     by 2^-14 of its size at the most (256 u M, M ~ 9), a sum of 64 of them by sqrt-free 64 * 2^-14 * |dy| = 2^-8 in the
