@@ -300,9 +300,10 @@ GSA_API int gsa_special_attention_noalloc_status(void *stream);
  * These calls create no context and allocate no memory: workspaces are the
  * caller's, one per call in flight (two calls that overlap on the GPU, or two
  * captured graphs that may run at the same time, need a workspace each).  All
- * pointers are device pointers of the current device, 16-byte aligned; calls
- * are asynchronous on `stream` and can be captured into a graph once one call
- * on the device has run outside a capture.  Sizes and lengths that the host
+ * pointers are device pointers of the current device, 16-byte aligned (arrays
+ * of int32, lse and weight gradients: 4 bytes); calls are asynchronous on
+ * `stream` and can be captured into a graph once one call on the device has run
+ * outside a capture.  Sizes and lengths that the host
  * does not know (cu_tokens, lengths, block tables) are read on the device and
  * checked there: what is out of range is left out and recorded, and
  * gsa_operator_status reports it.
@@ -378,7 +379,7 @@ typedef struct {
     int num_pages, page_size;     /* page_size 16, 32, 64, 128 or 256                 */
     int kv_heads;
     const int32_t *block_table;   /* [batch][max_pages], rows table_stride ints apart */
-    int batch, max_pages;
+    int batch, max_pages;         /* max_pages * page_size up to 2^31 - 257           */
     int64_t table_stride;
 } gsa_kv_cache;
 
@@ -409,7 +410,8 @@ GSA_API int gsa_cache_append(const gsa_kv_cache *cache, const gsa_norm_rope *op,
  *               left out and recorded); max_new * q heads / kv_heads up to 65535 * 64
  *   max_len   : about the longest of `lengths`; it only sets how the work is split
  *   softmax_scale : 0 for 1 / 8
- *   lse       : optional float32 [q heads][n_tokens], log-sum-exp of the scaled scores
+ *   lse       : optional float32 [q heads][n_tokens], log-sum-exp of the scaled scores;
+ *               written where out is
  *   workspace : gsa_cache_attention_workspace_bytes() of the same sizes
  * Pages outside the pool are left out as if masked, and recorded.  Memory that no
  * token stands in may hold anything.  A value that is not finite in a token of the
@@ -422,7 +424,8 @@ GSA_API size_t gsa_cache_attention_workspace_bytes(const gsa_kv_cache *cache, in
                                                    int max_new, int64_t max_len);
 
 /* Status of the operators on the current device: synchronises `stream`, returns
- * GSA_OK, GSA_ERR_DEVICE_BOUNDS or GSA_ERR_DEVICE_TIMEOUT and clears it. */
+ * GSA_OK, GSA_ERR_DEVICE_BOUNDS or GSA_ERR_DEVICE_TIMEOUT and clears it.  A timeout
+ * that has not been read lets later calls give up their waits early too. */
 GSA_API int gsa_operator_status(void *stream);
 
 #ifdef __cplusplus

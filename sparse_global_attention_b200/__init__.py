@@ -307,7 +307,8 @@ class GSALayer:
         the stored grid, queries and keys normed and rotated (qk_norm_rope) into the layer's layouts.
 
         positions: int32 [tokens, axes] or [frames, tokens, axes]; default: special tokens at (0, 0), the token of grid
-        row y and column x at (y + 1, x + 1); False: no rotation.  Returns the dict that forward() takes."""
+        row y and column x at (y + 1, x + 1) (made by the first such call, which has to be outside a capture); False: no
+        rotation.  Returns the dict that forward() takes."""
         from . import operators
         c, q, k, v, pos = self._qkv_parts(qkv, positions)
         kw = dict(norm=norm, eps=eps, q_weight=q_weight, q_bias=q_bias, k_weight=k_weight, k_bias=k_bias,
@@ -363,6 +364,8 @@ class GSALayer:
             raise GSAError(f"qkv must have the layer's type, got {qkv.dtype}")
         if positions is None:
             if self._grid_pos is None or self._grid_pos.device != qkv.device:
+                if torch.cuda.is_current_stream_capturing():
+                    raise GSAError("the default positions are made by the first call, outside a capture")
                 at = torch.arange(c.pad_h * c.pad_w, dtype=torch.int32)
                 grid = torch.stack([at // c.pad_w + 1, at % c.pad_w + 1], dim=1).to(torch.int32)
                 pos = torch.cat([torch.zeros(c.num_special, 2, dtype=torch.int32), grid])

@@ -41,6 +41,7 @@ int status_words(int** out) {
 size_t esize(int dtype) { return dtype == GSA_BF16 ? 2 : 4; }
 bool is_dtype(int dtype) { return dtype == GSA_BF16 || dtype == GSA_FP32; }
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 // Rows of n_outer x n_tokens tokens.  Written rows may not lie on one another: a
 // stride of zero is refused where there is more than one.
@@ -101,7 +102,7 @@ int check_affine(const gsa_norm_rope* op, const void* w, const void* b) {
 int check_positions(const gsa_norm_rope* op, const int32_t* pos, int64_t n_outer, int64_t so, bool may_lack) {
   if (op->rope_axes == 0) return pos ? GSA_ERR_INVALID_ARG : GSA_OK;
   if (!pos) return may_lack && op->rope_axes == 1 ? GSA_OK : GSA_ERR_INVALID_ARG;
-  if ((reinterpret_cast<uintptr_t>(pos) & 3u) || (n_outer > 1 && so < 0)) return GSA_ERR_INVALID_ARG;
+  if (!aligned4(pos) || (n_outer > 1 && so < 0)) return GSA_ERR_INVALID_ARG;
   return GSA_OK;
 }
 
@@ -118,9 +119,10 @@ int check_cache(const gsa_kv_cache* c) {
   if (static_cast<int64_t>(c->num_pages) * c->kv_heads * c->page_size >= (1LL << 31)) return GSA_ERR_UNSUPPORTED;
   if (!c->k_pages || !c->v_pages || !aligned16(c->k_pages) || !aligned16(c->v_pages)) return GSA_ERR_INVALID_ARG;
   if (c->batch > 0 && c->max_pages > 0 &&
-      (!c->block_table || (reinterpret_cast<uintptr_t>(c->block_table) & 3u) ||
-       (c->batch > 1 && c->table_stride < c->max_pages)))
+      (!c->block_table || !aligned4(c->block_table) || (c->batch > 1 && c->table_stride < c->max_pages)))
     return GSA_ERR_INVALID_ARG;
+  // places in a sequence, rounded up to a tile of keys, are counted in 32 bits
+  if (static_cast<int64_t>(c->max_pages) * c->page_size > 0x7fffffff - 256) return GSA_ERR_UNSUPPORTED;
   return GSA_OK;
 }
 
@@ -213,6 +215,7 @@ extern "C" int gsa_qk_norm_rope_backward(const gsa_norm_rope* op, int grad_dtype
     if (i < 2 && (dw[i] || db[i])) {
       // sums of a tensor that is not there, of no norm, or a bias that the norm has not
       if (!go[i] || op->norm == GSA_NORM_NONE || (db[i] && op->norm != GSA_NORM_LAYER)) return GSA_ERR_INVALID_ARG;
+      if (!aligned4(dw[i]) || !aligned4(db[i])) return GSA_ERR_INVALID_ARG;
       sums = true;
     }
     if (!go[i]) continue;
@@ -263,7 +266,7 @@ extern "C" int gsa_cache_append(const gsa_kv_cache* cache, const gsa_norm_rope* 
   if (k->heads != cache->kv_heads || v->heads != cache->kv_heads) return GSA_ERR_SHAPE;
   GSA_TRY(check_affine(op, k_weight, k_bias));
   if (n_tokens == 0 || cache->batch == 0) return GSA_OK;
-  if (!cu_tokens || !start) return GSA_ERR_INVALID_ARG;
+  if (!cu_tokens || !start || !aligned4(cu_tokens) || !aligned4(start)) return GSA_ERR_INVALID_ARG;
   GSA_TRY(check_positions(op, positions, 1, 0, true));
   int* words = nullptr;
   GSA_TRY(status_words(&words));
@@ -321,7 +324,7 @@ extern "C" int gsa_cache_attention(const gsa_kv_cache* cache, int64_t n_tokens, 
   if (out->heads != q->heads) return GSA_ERR_SHAPE;
   if (!(softmax_scale >= 0.f) || isinf(softmax_scale)) return GSA_ERR_INVALID_ARG;
   if (n_tokens == 0 || cache->batch == 0 || max_new == 0) return GSA_OK;
-  if (!cu_tokens || !lengths) return GSA_ERR_INVALID_ARG;
+  if (!cu_tokens || !lengths || !aligned4(cu_tokens) || !aligned4(lengths) || !aligned4(lse)) return GSA_ERR_INVALID_ARG;
   const bool fp32 = cache->dtype == GSA_FP32;
   const CacheAttnPlan p =
       plan_cache_attn(fp32, cache->batch, cache->kv_heads, q->heads, n_tokens, max_new, max_len);

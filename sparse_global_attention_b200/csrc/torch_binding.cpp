@@ -75,6 +75,15 @@ int small(PyObject* o, const char* name) {
   return static_cast<int>(v);
 }
 
+bool truth(PyObject* o, const char* name) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) {
+    PyErr_Clear();
+    refuse(name, " must be true or false");
+  }
+  return v == 1;
+}
+
 int gsa_type(at::ScalarType t) {
   return t == at::kBFloat16 ? GSA_BF16 : t == at::kFloat ? GSA_FP32 : -1;
 }
@@ -93,7 +102,10 @@ struct On {
   void* stream;
   On(c10::Device dev, PyObject* given) : device(dev) {
     if (given != Py_None) {
-      auto* h = reinterpret_cast<cudaStream_t>(integer(given, "stream"));
+      const int64_t raw = integer(given, "stream");
+      // 1 and 2 name default streams by their kind, which the allocator's bookkeeping does not know
+      if (raw == 1 || raw == 2) refuse("stream must be 0 or the handle of a stream, got ", raw);
+      auto* h = reinterpret_cast<cudaStream_t>(raw);
       guard.emplace(c10::cuda::getStreamFromExternal(h, dev.index()));
       stream = h;
     } else {
@@ -154,15 +166,20 @@ Positions positions(const at::Tensor* t, const Shape& s, c10::Device dev) {
   return r;
 }
 
-PyObject* item(PyObject* out, Py_ssize_t i) {      // of `out`: None, or a sequence of three
-  if (out == Py_None) return Py_None;
-  PyObject* o = PySequence_Check(out) && PySequence_Size(out) == 3 ? PySequence_GetItem(out, i) : nullptr;
-  if (!o) {
+// tensor i of `out`: None, or a sequence of three tensors or Nones.  A sequence may make its items
+// as they are asked for (a tensor of three does), so the item is held until its tensor is.
+at::Tensor item(PyObject* out, Py_ssize_t i, const char* name) {
+  if (out == Py_None) return at::Tensor();
+  struct Held {
+    PyObject* o;
+    ~Held() { Py_XDECREF(o); }
+  } held{PySequence_Check(out) && PySequence_Size(out) == 3 ? PySequence_GetItem(out, i) : nullptr};
+  if (!held.o) {
     PyErr_Clear();
     refuse("out must be three tensors or Nones");
   }
-  Py_DECREF(o);                                    // the caller's sequence keeps it
-  return o;
+  const at::Tensor* t = tensor(held.o, name);
+  return t ? *t : at::Tensor();
 }
 
 PyObject* wrap(const at::Tensor& t) {
@@ -205,7 +222,7 @@ PyObject* norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const auto dev = first->device();
     if (gsa_type(type) < 0) refuse("q, k, v must be bfloat16 or float32, got ", type);
     On on(dev, a[13]);
-    const bool head_major = PyObject_IsTrue(a[11]) == 1;
+    const bool head_major = truth(a[11], "head_major");
     Shape s;
     gsa_rows ri[3], ro[3];
     const gsa_rows *pi[3] = {}, *po[3] = {};
@@ -214,9 +231,8 @@ PyObject* norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
       if (!in[i]) continue;
       ri[i] = rows4(*in[i], names[i], type, dev, false, s, -1);
       const int64_t heads = ri[i].heads;
-      if (const at::Tensor* o = tensor(item(a[12], i), outs[i]))
-        res[i] = *o;
-      else
+      res[i] = item(a[12], i, outs[i]);
+      if (!res[i].defined())
         res[i] = head_major ? make({heads, s.outer, s.tokens, DIM}, type, dev) : make({s.outer, s.tokens, heads, DIM}, type, dev);
       ro[i] = rows4(res[i], outs[i], type, dev, head_major, s, heads);
       pi[i] = &ri[i];
@@ -261,7 +277,7 @@ PyObject* norm_rope_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int norm = small(a[5], "norm");
     const bool normed = norm != GSA_NORM_NONE;
     On on(dev, a[15]);
-    const bool head_major = PyObject_IsTrue(a[13]) == 1;
+    const bool head_major = truth(a[13], "head_major");
     Shape s;
     gsa_rows rx[2], rg[3], rd[3];
     const gsa_rows *px[2] = {}, *pg[3] = {}, *pd[3] = {};
@@ -282,10 +298,8 @@ PyObject* norm_rope_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
           ps[2 * i + b] = sums[2 * i + b].data_ptr<float>();
         }
       }
-      if (const at::Tensor* o = tensor(item(a[14], i), outs[i]))
-        res[i] = *o;
-      else
-        res[i] = make({s.outer, s.tokens, heads, DIM}, gtype, dev);
+      res[i] = item(a[14], i, outs[i]);
+      if (!res[i].defined()) res[i] = make({s.outer, s.tokens, heads, DIM}, gtype, dev);
       rd[i] = rows4(res[i], outs[i], gtype, dev, false, s, heads);
       pd[i] = &rd[i];
     }
@@ -392,12 +406,12 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (const at::Tensor* o = tensor(a[11], "out")) out = *o;
     else out = make({tokens, q.size(1), DIM}, type, dev);
     const gsa_rows ro = rows3(&out, "out", type, dev, &q);
-    if (PyObject_IsTrue(a[10]) == 1) lse = make({q.size(1), tokens}, at::kFloat, dev);
+    if (truth(a[10], "return_lse")) lse = make({q.size(1), tokens}, at::kFloat, dev);
     const size_t bytes = g_lib.attention_bytes(&c, tokens, rq.heads, max_new, max_len);
     if (bytes) ws = make({static_cast<int64_t>(bytes)}, at::kByte, dev);
     check(g_lib.attention(&c, tokens, &rq, &ro, ints(tensor(a[5], "cu_tokens"), "cu_tokens", c.batch + 1ll, dev),
                           ints(tensor(a[4], "lengths"), "lengths", c.batch, dev), max_new, max_len,
-                          PyObject_IsTrue(a[8]) == 1, static_cast<float>(number(a[9], "softmax_scale")),
+                          truth(a[8], "causal"), static_cast<float>(number(a[9], "softmax_scale")),
                           lse.defined() ? lse.data_ptr<float>() : nullptr, bytes ? ws.data_ptr() : nullptr, bytes,
                           on.stream),
           "gsa_cache_attention");

@@ -124,6 +124,7 @@ class KVCache:
         0 .. lengths[b] - 1, or with `causal` (they are then its last ones) up to their own.  Query heads are a multiple
         of the cache's heads.  max_new: at least the most new tokens of a sequence.  max_len: about the longest of
         `lengths` (default: what the block table can hold); it only sets how the work is split.  softmax_scale 0: 1 / 8.
-        Returns out (rows from cu_tokens[-1] on untouched), with return_lse also float32 [query heads, tokens]."""
+        Returns out (rows from cu_tokens[-1] on untouched), with return_lse also float32 [query heads, tokens] (columns
+        from cu_tokens[-1] on not written)."""
         return _b.attention(self.k_pages, self.v_pages, q, block_table, lengths, cu_tokens, max_new, max_len, causal,
                             softmax_scale, return_lse, out, stream)

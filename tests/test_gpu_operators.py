@@ -679,6 +679,70 @@ def test_layer_inputs_from_a_projection(cfg):
         layer.close()
 
 
+def test_default_positions_are_made_outside_a_capture():
+    cfg = SMALL
+    qkv = torch.randn(cfg.num_frames, cfg.num_special + cfg.pad_h * cfg.pad_w, 3, cfg.num_heads, 64, device="cuda")
+    qkv = qkv.to(TYPES[cfg.dtype])
+    layer = gsa.GSALayer.from_workload(cfg)
+    try:
+        one = torch.ones(3, device="cuda")
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            two = one + 1
+            with pytest.raises(gsa.GSAError, match="capture"):
+                layer.split_qkv(qkv, None, norm="none")
+        graph.replay()
+        assert (two == 2).all()
+        want = layer.split_qkv(qkv, None, norm="none")
+        with torch.cuda.graph(graph2 := torch.cuda.CUDAGraph()):
+            got = layer.split_qkv(qkv, None, norm="none")
+        graph2.replay()
+        assert all(torch.equal(got[n], want[n]) for n in want if n != "w_g")
+    finally:
+        layer.close()
+
+
+def test_outputs_from_a_sequence_that_makes_its_items():
+    """`out` may be any sequence of three, also one whose items nothing else holds."""
+    class Parts:
+        def __init__(self, whole):
+            self.whole = whole
+
+        def __len__(self):
+            return len(self.whole)
+
+        def __getitem__(self, i):
+            return self.whole[i]
+
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = [torch.randn(2, 9, 4, 64, generator=g, device="cuda") for _ in range(3)]
+    pos = torch.arange(9, dtype=torch.int32, device="cuda")[:, None]
+    want = gsa.qk_norm_rope(*x, norm="none", positions=pos)
+    room = torch.zeros(3, 2, 9, 4, 64, device="cuda")
+    got = gsa.qk_norm_rope(*x, norm="none", positions=pos, out=Parts(room))
+    assert all(torch.equal(a, b) and torch.equal(a, r) for a, b, r in zip(got, want, room))
+    back = torch.zeros_like(room)
+    r = gsa.qk_norm_rope_backward(None, None, *want, norm="none", positions=pos, out=Parts(back))
+    again = gsa.qk_norm_rope_backward(None, None, *want, norm="none", positions=pos)
+    assert all(torch.equal(r[n], again[n]) and torch.equal(r[n], b) for n, b in zip(("dq", "dk", "dv"), back))
+    for bad in (room, Parts(room[:2]), "abc", 3, [1, 2, 3]):
+        with pytest.raises(gsa.GSAError):
+            gsa.qk_norm_rope(*x, norm="none", positions=pos, out=bad)
+
+
+def test_arguments_that_are_no_truth_values_or_streams():
+    x = torch.randn(2, 9, 4, 64, device="cuda")
+    for kw in (dict(head_major=torch.zeros(2)), dict(stream=1), dict(stream=2), dict(stream="a")):
+        with pytest.raises(gsa.GSAError):
+            gsa.qk_norm_rope(x, norm="none", **kw)
+    s = Streams([1], [3], 16, 1, torch.float32)
+    q = s.rand(1, 1)
+    for kw in (dict(causal=torch.zeros(2)), dict(return_lse=torch.zeros(2))):
+        with pytest.raises(gsa.GSAError):
+            s.cache.attention(q, s.table, s.lengths, s.cu, 1, **kw)
+    clean()
+
+
 # ---- streams and graphs ------------------------------------------------------------------------
 def test_two_streams_at_once():
     """The same calls on two streams at the same time: no workspace is shared."""

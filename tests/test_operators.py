@@ -138,6 +138,22 @@ def test_attention_workspace_bytes():
     assert size(_cache(batch=64), 64 * 2000, 4, 2000, 2000) == 0    # enough rows
 
 
+def test_lengths_and_places_beyond_32_bits():
+    size = lambda cache, *a: _fn("gsa_cache_attention_workspace_bytes", cache, *a)
+    for batch in (1, 3):                                     # a length is never longer than 2^31 - 1
+        assert size(_cache(batch=batch), batch, 4, 1, (1 << 63) - 1) == size(_cache(batch=batch), batch, 4, 1, (1 << 31) - 1) > 0
+    wide = _cache(page=256, most=(1 << 23) - 1, stride=1 << 23)      # places up to 2^31 - 256 are one tile too many
+    assert _append(cache=wide) == 3 and _attention(cache=wide) == 3
+
+
+@pytest.mark.parametrize("call", [
+    lambda: _append(cu=P + 2), lambda: _append(start=P + 1), lambda: _append(cache=_cache(table=P + 2)),
+    lambda: _attention(cu=P + 2), lambda: _attention(lens=P + 2), lambda: _attention(lse=P + 2),
+    lambda: _backward(sums=(P + 2, None, None, None)), lambda: _backward(sums=(P, P + 1, None, None))])
+def test_arrays_of_32_bits_are_aligned(call):
+    assert call() == 1
+
+
 @pytest.mark.parametrize("norm", ["none", "layer", "rms"])
 @pytest.mark.parametrize("axes", [0, 1, 2])
 def test_oracle_gradients_against_differences(norm, axes):
