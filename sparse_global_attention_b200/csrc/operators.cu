@@ -89,7 +89,8 @@ void make_table(const gsa_norm_rope* op, RopeTable* t) {
   const int half = 32 / op->rope_axes;
   const long double ratio = powl(op->rope_base, -1.0L / half);
   long double f = 1.0L / 6.283185307179586476925286766559L;
-  for (int i = 0; i < half; ++i, f *= ratio) t->f[i] = static_cast<unsigned long long>(ldexpl(f - floorl(f), 64));
+  for (int i = 0; i < half; ++i, f *= ratio)
+    t->f[i] = static_cast<unsigned long long>((f < 1.0L ? f : f - floorl(f)) * 0x1p64L);
 }
 
 // weight and bias of one normed tensor
