@@ -289,6 +289,10 @@ __global__ void __launch_bounds__(Lay<KIND>::NTHREADS, KIND == QUARTERS ? 2 : 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   allow_join();
+  if (threadIdx.x == 32 * L::NWARP) {              // while the sequence is looked up
+    prefetch_tmap(&tm_k);
+    prefetch_tmap(&tm_v);
+  }
   const Block blk = block_of<L::ROWS, TN>(a);
   if (!blk.any) return;
   if (sbase & 1023u) {                            // the operands' swizzle needs it
