@@ -687,10 +687,24 @@ __global__ void __launch_bounds__(Lay<KIND>::NTHREADS, KIND == QUARTERS ? 2 : 1)
 
 // ---- fp32 ---------------------------------------------------------------------
 // 64 rows by 64 keys per step, 256 threads as 16 x 16: thread (ty, tx) holds 4 rows by
-// 4 keys (tx + 16 i) of S and the same rows by channels 4 tx .. of O.
+// 4 keys (tx + 16 i) of S and the same rows by channels 4 tx .. of O.  Scores take two channels in
+// one instruction (their operands lie side by side; in P V they would have to be moved together,
+// which made it 13 % slower).  512 queries of 37 heads over 8192 keys, 296 full blocks: 34
+// TFLOP/s, 46 % of the FMA pipe (33 with single products); 4 or 8 rows by 8 keys per thread, which
+// read half the shared memory (32 % of its rate instead of 62 %), reached 33 as well: what is left is
+// the warps' waits for each step's loads and for the softmax between the two products.
 constexpr int FK = 64;                    // keys per tile
 constexpr int FP = 68;                    // row pitch in floats: 16-byte reads of 16 rows meet no bank twice
 constexpr int TR = 64;
+// two products and sums in one instruction
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n .reg .b64 a, b, c;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mov.b64 c, {%6, %7};\n"
+      " fma.rn.f32x2 a, a, b, c;\n mov.b64 {%0, %1}, a;\n}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
 // four channels of a row's result, or of this split's part
 __device__ __forceinline__ void write_f32(const CacheAttnArgs& a, const Block& blk, int at, int head, int e0, float4 o,
                                           float m, float l) {
@@ -785,10 +799,11 @@ __global__ void __launch_bounds__(256, 2) cache_attn_f32_kernel(const __grid_con
     const float* k = sk + buf * FK * FP;
     const float* v = sv + buf * FK * FP;
     float s[R][4];
+    float2 s2[R][4];
 #pragma unroll
     for (int i = 0; i < R; ++i)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[i][e] = 0.f;
+      for (int e = 0; e < 4; ++e) s2[i][e] = make_float2(0.f, 0.f);
 #pragma unroll 4
     for (int d = 0; d < D; d += 4) {
       float4 kv[4];
@@ -799,10 +814,8 @@ __global__ void __launch_bounds__(256, 2) cache_attn_f32_kernel(const __grid_con
         const float4 q = *reinterpret_cast<const float4*>(sq + (ty * R + i) * FP + d);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          s[i][e] = fmaf(q.x, kv[e].x, s[i][e]);
-          s[i][e] = fmaf(q.y, kv[e].y, s[i][e]);
-          s[i][e] = fmaf(q.z, kv[e].z, s[i][e]);
-          s[i][e] = fmaf(q.w, kv[e].w, s[i][e]);
+          s2[i][e] = fma2(make_float2(q.x, q.y), make_float2(kv[e].x, kv[e].y), s2[i][e]);
+          s2[i][e] = fma2(make_float2(q.z, q.w), make_float2(kv[e].z, kv[e].w), s2[i][e]);
         }
       }
     }
@@ -814,6 +827,7 @@ __global__ void __launch_bounds__(256, 2) cache_attn_f32_kernel(const __grid_con
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int key = tx + 16 * e;
+        s[i][e] = s2[i][e].x + s2[i][e].y;
         if (kb + key >= lim[i] || !skey[buf * FK + key]) s[i][e] = -INFINITY;
         mx = fmaxf(mx, s[i][e]);
       }
