@@ -17,7 +17,8 @@
 // fixed order (S and P V of one stream, then of the other) keeps them out of step, which an
 // issuer for each stream did not (1183 against 977 us, 1301 queries of 16 heads over 83,264
 // keys, one block per 256 rows), nor turns taken by barriers (1000), three streams
-// of 64-key tiles (1404), or reading the next scores under the exponentials (1464).  3 of
+// of 64-key tiles (1404), or reading the next scores under the exponentials (1464).  (With two
+// warps per 32 rows and the keys split over three blocks the call takes 640 to 660.)  3 of
 // 16 exponentials run on the FMA pipe (913 against 924 us; 4 of 16: 961).
 // Variants by the rows of a sequence and key head:
 //   ROW_TILES (a chunk of tokens): the streams are two row tiles over the same keys;

@@ -391,6 +391,8 @@ __global__ void __launch_bounds__(NTHR, 3) norm_rope_kernel(const __grid_constan
 // time, with its own angles (four a lane).  No lane is left without a row whatever the heads are, and
 // the angles cost a token, not a head; but a warp holds four tokens and has to go through all their
 // heads, which makes small calls longer.  launch_fwd has the rule between the two and its figures.
+// Three blocks an SM: two, with the next rows on their way while a warp works on these, took 378 us
+// for the 128 frames where this takes 364, items of at most eight heads 387.
 template <typename T, int NORM, int AXES, bool PAGED>
 __global__ void __launch_bounds__(NTHR, 3) norm_rope_group_kernel(const __grid_constant__ NormRopeArgs a) {
   const int lane = threadIdx.x & 31, r = lane >> 3;
