@@ -1198,25 +1198,27 @@ CacheAttnPlan plan_cache_attn(bool fp32, int batch, int kv_heads, int q_heads, l
   CacheAttnPlan p;
   const long long most = n_tokens < max_new ? n_tokens : max_new;
   const long long rows = most * (q_heads / kv_heads);
-  // Per variant: rows and keys of a tile, blocks that run at once, key tiles worth a split, and
-  // measured times in us: a key tile of a block alone and with all SMs at work, a block's start.
+  // Per variant: rows and keys of a tile, blocks that run at once, and times in us: a key tile of a
+  // block alone and with all SMs at work, a block's start.  The times, and those of rounds and join
+  // below, are fitted to a sweep of 650 calls of drawn sizes with 1 to 96 parts each: the chosen
+  // number of parts takes 3 to 4 % longer than the best one in the mean (one part: 60 %).
   struct Cost {
-    int tile, keys, slots, least;
+    int tile, keys, slots;
     double alone, busy, start;
   };
-  static const Cost costs[] = {{256, 128, 148, 16, 1.4, 1.4, 4.0},       // ROW_TILES
-                               {128, 128, 148, 2, 0.36, 0.75, 5.0},      // ONE_TILE
-                               {32, 128, 296, 2, 0.55, 1.45, 4.0},       // QUARTERS
-                               {64, 64, 296, 1, 5.8, 6.2, 4.0},          // F32_64
-                               {8, 64, 296, 2, 2.0, 2.2, 3.0},           // F32_8
-                               {4, 64, 296, 2, 1.3, 1.5, 3.0}};          // F32_4
+  static const Cost costs[] = {{256, 128, 148, 1.3, 2.3, 4.5},      // ROW_TILES
+                               {128, 128, 148, 0.7, 0.8, 5.0},      // ONE_TILE
+                               {32, 128, 296, 0.9, 2.3, 5.5},       // QUARTERS
+                               {64, 64, 296, 5.9, 10.0, 3.0},       // F32_64
+                               {8, 64, 296, 2.4, 3.5, 3.0},         // F32_8
+                               {4, 64, 296, 0.95, 2.6, 3.5}};       // F32_4
   p.kind = fp32 ? (rows <= 4 ? F32_4 : rows <= 24 ? F32_8 : F32_64) : (rows <= 32 ? QUARTERS : rows <= 128 ? ONE_TILE : ROW_TILES);
   const Cost& c = costs[p.kind];
   if (max_len > 0x7fffffff) max_len = 0x7fffffff;          // no sequence is longer
   p.row_tiles = static_cast<int>((rows + c.tile - 1) / c.tile);
   if (p.row_tiles < 1) p.row_tiles = 1;
   const long long ktiles = (max_len + c.keys - 1) / c.keys;
-  long long ns = 1, most_splits = ktiles / c.least;
+  long long ns = 1, most_splits = ktiles;
   if (most_splits > 128) most_splits = 128;
   if (most_splits > 1) {
     // The blocks that have rows (a block with one of its two row tiles takes four fifths of the
@@ -1226,22 +1228,20 @@ CacheAttnPlan plan_cache_attn(bool fp32, int batch, int kv_heads, int q_heads, l
     const double group = static_cast<double>(q_heads) / kv_heads;
     const long long units = (rows * half + c.tile - 1) / c.tile;
     double blocks = static_cast<double>(units / half) + (units % half ? 0.8 : 0.0);
-    if (batch > 1 && n_tokens * group / c.tile + 0.5 * batch < blocks * batch)
-      blocks = n_tokens * group / c.tile + 0.5 * batch;
-    else
-      blocks *= batch;
+    blocks *= batch;
+    if (batch > 1) blocks = fmin(blocks, fmax(n_tokens * group / c.tile + 0.5 * batch, batch));
     blocks *= kv_heads;
-    const double mean = batch > 1 ? 0.85 : 1.0;
+    const double mean = batch > 1 ? 0.9 : 1.0;
     double best = 1e30;
     // (more than a round and a half of blocks: their order evens them out, and parts only cost)
     for (long long n = 1; n <= most_splits && (n == 1 || blocks < 1.5 * c.slots); ++n) {
       const double chunk = ceil(static_cast<double>(ktiles) / n);
       const double run = blocks * (mean * n + (n > 1 ? 0.5 * (1.0 - mean) : 1.0 - mean));       // blocks with keys
       const double r = run / c.slots;
-      const double rounds = r <= 1.0 ? 1.0 : batch > 1 ? fmin(r + 0.6, 2.0 * r - 1.0) : ceil(r);
+      const double rounds = r <= 1.0 ? 1.0 : batch > 1 ? fmin(r + 0.3, 1.0 + 2.1 * (r - 1.0)) : ceil(r);
       const double tile_us = c.alone + (c.busy - c.alone) * (r < 1.0 ? r : 1.0);
       // joining: a launch, and the parts written and read once
-      const double join = n > 1 ? 4.4 + n * (0.08 + n_tokens * q_heads * 1e-4) : 0.0;
+      const double join = n > 1 ? 2.0 + n * (0.07 + n_tokens * q_heads * 1e-4) : 0.0;
       const double t = rounds * (chunk * tile_us + 0.5 * c.start) + 0.5 * c.start + join;
       if (t < best * 0.95) {
         best = t;
