@@ -897,9 +897,9 @@ __global__ void __launch_bounds__(256, 2) cache_attn_f32_kernel(const __grid_con
 // 8 shuffles for 8 keys), so that lane c ends with the score of key 2 (c / (16 / N)) + half; the
 // weights are handed back by shuffles for O += p V.  Each warp has its own running maximum and
 // sums; the block's eight warps are joined at the end.  A step's keys lie in one page.  16 rows by
-// 64 keys through shared memory (one row a thread) read 1.6 TB/s where this reads 4.9 (48
-// sequences of 9728 tokens, single new ones, 4 key heads and 16 query heads: 0.96 GB in 194 us; one
-// query head for each key head 162 us, 5.9 TB/s).
+// 64 keys through shared memory (one row a thread) read 1.6 TB/s where this reads 5.6 (48
+// sequences of 9728 tokens, single new ones, 4 key heads and 16 query heads: 0.96 GB in 170 us; one
+// query head for each key head 151 us, 6.3 TB/s).
 template <int R, int N>
 __global__ void __launch_bounds__(256, 2) cache_attn_f32_few_kernel(const __grid_constant__ CacheAttnArgs a) {
   constexpr int KEYS = 2 * N, WARPS = 8, PART = 66;
