@@ -549,13 +549,15 @@ __global__ void __launch_bounds__(Lay<KIND>::NTHREADS, KIND == QUARTERS ? 2 : 1)
           if (half == 0) mx = *xch;
         }
         const float m_new = fmaxf(m, mx);
-        const bool need = (m == -INFINITY) ? (m_new != -INFINITY) : ((m_new - m) * sl2 > RESCALE_LOG2);
+        const bool had = m != -INFINITY;             // a row without a key so far has nothing in O
+        const bool need = had ? (m_new - m) * sl2 > RESCALE_LOG2 : m_new != -INFINITY;
         if (need) {
-          alpha = (m == -INFINITY) ? 0.f : ex2((m - m_new) * sl2);
+          alpha = had ? ex2((m - m_new) * sl2) : 0.f;
           m = m_new;
         }
         l *= alpha;
-        grow = __any_sync(0xffffffffu, need && alpha != 0.f);
+        // by a factor of 0 too: past a rise of 126 (log2 units) nothing of O is left
+        grow = __any_sync(0xffffffffu, need && had);
       }
       // P (and O) are free once the previous tile's product has completed
       if (n > 0) {

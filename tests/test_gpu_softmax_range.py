@@ -1,0 +1,64 @@
+"""Online softmax over scores whose running maximum moves far: between two key tiles
+the factor that brings the sums so far to the new maximum, 2^((old - new) log2 e scale),
+can underflow to zero, and the output so far has to be multiplied by that zero as the
+sum of the weights is.
+
+Keys lie along (1, .., 1) at a level of their own group of places, so a group's scaled
+scores are 8 * level * query, and each group's values have a mean of their own: a group
+that stays in the output although its weight is gone moves it by the means' distance.
+Tolerances: those of test_gpu_operators."""
+import pytest
+import torch
+
+from test_gpu_operators import TYPES, Streams, check_attention, clean
+
+pytestmark = pytest.mark.gpu
+
+# (places up to which a level holds, as parts of the length; levels in 32nds, a quarter of which is a unit query's scaled score)
+RISING = ((0.31, 0.72, 1.0), (-800, -100, 400))         # -200, -25, 100
+FALLING = ((0.31, 0.72, 1.0), (400, -100, -800))
+JUST = ((0.31, 0.72, 1.0), (-200, 0, 240))              # -50, 0, 60: factors of 2^-72 and 2^-87, no underflow
+LATE = ((0.93, 1.0), (-480, 480))                       # -120, 120: 2^-346
+
+
+def levels(length, steps, device="cuda"):
+    at = torch.arange(length, device=device)
+    ends, values = steps
+    k = torch.full((length,), values[-1] / 32.0, device=device)
+    for e, v in reversed(list(zip(ends, values))):
+        k[at < round(e * length)] = v / 32.0
+    return k
+
+
+def keys_and_values(g, length, heads, steps, dtype):
+    """Keys at their levels, and values 5, 1, -3 (by the group of places) with noise."""
+    k = levels(length, steps)
+    mean = torch.full((length,), 5.0, device="cuda")
+    for i, e in enumerate(steps[0][:-1]):
+        mean[torch.arange(length, device="cuda") >= round(e * length)] = 1.0 - 4.0 * i
+    noise = torch.randn(length, heads, 64, generator=g, device="cuda")
+    near = torch.randn(length, heads, 64, generator=g, device="cuda") / 16       # scores of a group spread by 1/16
+    return (k[:, None, None] + near).to(dtype), (mean[:, None, None] + 0.5 * noise).to(dtype)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("steps", [RISING, FALLING, JUST, LATE], ids=["rising", "falling", "just", "late"])
+@pytest.mark.parametrize("rows", ["same", "mixed"])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("n,hk,group", [(1, 2, 1), (1, 2, 4), (5, 1, 3), (50, 2, 1), (300, 1, 1), (100, 1, 5)])
+def test_cache_attention_when_the_maximum_moves_far(n, hk, group, dtype, rows, steps, causal):
+    dt, lengths = TYPES[dtype], [1100, 777]
+    s = Streams([n, n], [t - n for t in lengths], 16, hk, dt, seed=n + group)
+    parts = [keys_and_values(s.g, t, hk, steps, dt) for t in lengths]
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    s.cache.append(torch.cat([k for k, _ in parts]), torch.cat([v for _, v in parts]), s.table, i32([0, 0]),
+                   i32([0, lengths[0], sum(lengths)]))
+    q = torch.ones(2 * n, hk * group, 64, device="cuda")
+    if rows == "mixed":      # in one warp rows whose maximum rises, falls and stays
+        q *= torch.tensor([1.0, -1.0, 0.25, 0.0], device="cuda")[torch.arange(q.shape[0] * q.shape[1], device="cuda") % 4].view(
+            q.shape[0], -1, 1)
+    q = q.to(dt)
+    for max_len in (1, 300, 200000):           # one part, and several
+        out, lse = s.cache.attention(q, s.table, s.lengths, s.cu, n, max_len=max_len, causal=causal, return_lse=True)
+        check_attention(s, q, out, lse, causal)
+    clean()
