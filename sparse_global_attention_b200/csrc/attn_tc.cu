@@ -202,14 +202,16 @@ template <int PIECE>
 __device__ __forceinline__ void rescale(float mx, float& m, float& l, int j, int qi, uint32_t tO,
                                         const Bars& bars, int* err, bool& ok, float sl2) {
   const float m_new = fmaxf(m, mx);
-  const bool need = (m == -INFINITY) ? (m_new != -INFINITY) : ((m_new - m) * sl2 > RESCALE_LOG2);
+  const bool had = m != -INFINITY;                 // a row without a key so far has nothing in O
+  const bool need = had ? (m_new - m) * sl2 > RESCALE_LOG2 : m_new != -INFINITY;
   float alpha = 1.f;
   if (need) {
-    alpha = (m == -INFINITY) ? 0.f : ex2((m - m_new) * sl2);
+    alpha = had ? ex2((m - m_new) * sl2) : 0.f;
     m = m_new;
   }
   l *= alpha;
-  if (__any_sync(0xffffffffu, need && alpha != 0.f) && j > 0) {
+  // by a factor of 0 too: past a rise of 126 (log2 units) nothing of O is left
+  if (__any_sync(0xffffffffu, need && had) && j > 0) {
     ok = __all_sync(0xffffffffu, mbar_wait(bars.pv_done(qi), (j - 1) & 1, err));
     if (!ok) return;
     tc_fence_after();

@@ -6,10 +6,14 @@ sum of the weights is.
 Keys lie along (1, .., 1) at a level of their own group of places, so a group's scaled
 scores are 8 * level * query, and each group's values have a mean of their own: a group
 that stays in the output although its weight is gone moves it by the means' distance.
-Tolerances: those of test_gpu_operators."""
+Tolerances: those of test_gpu_operators (attention over the cache) and of gpu_helpers (the layer)."""
 import pytest
 import torch
 
+import oracle
+import sparse_global_attention_b200 as gsa
+from gpu_helpers import assert_close, compare_head, run_gpu
+from gsa_inputs import GSAConfig, make_inputs, to_f64_numpy
 from test_gpu_operators import TYPES, Streams, check_attention, clean
 
 pytestmark = pytest.mark.gpu
@@ -62,3 +66,62 @@ def test_cache_attention_when_the_maximum_moves_far(n, hk, group, dtype, rows, s
         out, lse = s.cache.attention(q, s.table, s.lengths, s.cu, n, max_len=max_len, causal=causal, return_lse=True)
         check_attention(s, q, out, lse, causal)
     clean()
+
+
+# ---- the layer's kernels --------------------------------------------------------------------
+WIDE = GSAConfig("wide_bf16", 6, 24, 24, 24, 24, 5, 2, 64, 4, 32, "bf16")      # R = 216 regions: two key tiles
+FIXED = GSAConfig("wide_fixed_bf16", 6, 24, 24, 24, 24, 5, 2, 64, 4, 16, "bf16", (0, 4))
+
+
+def layer_inputs(cfg, low, high, value):
+    """Queries near one; keys at `low` in the first frames and at `high` in the last ones (`value` the frame and the
+    region row that they begin at), values 1 and -1 with noise (small: the bar on the outputs is absolute)."""
+    frame, rows = value
+    x = {k: v.float() for k, v in make_inputs(cfg, seed=2).items()}
+    g = torch.Generator().manual_seed(5)
+    late = torch.zeros(cfg.num_frames, cfg.pad_h, 1, 1)
+    late[frame + 1:] = 1
+    late[frame, 4 * rows:] = 1
+    spec = torch.zeros(cfg.num_frames, 1, 1)
+    spec[frame:] = 1
+    for part, at in (("img", late), ("spec", spec)):
+        noise = lambda: torch.randn(x["q_" + part].shape, generator=g)
+        x["q_" + part] = 1 + noise() / 8
+        x["k_" + part] = low + (high - low) * at + noise() / 8
+        x["v_" + part] = 1 - 2 * at + noise() / 8
+    return {k: v.bfloat16().cuda() for k, v in x.items()}
+
+
+JUMPS = [(-25.0, 12.5, (4, 0)),       # scores -200 and 100, from region 144 on: inside the second tile
+         (-25.0, 12.5, (5, 2)),       # from region 192 on: the second half of that tile
+         (-6.25, 7.5, (4, 0)),        # -50 and 60: 2^-159
+         (-4.0, 4.0, (4, 0)),         # -32 and 32: 2^-92, no underflow
+         (12.5, -25.0, (4, 0))]       # falling
+
+
+@pytest.mark.parametrize("low,high,value", JUMPS)
+@pytest.mark.parametrize("cfg", [WIDE, FIXED], ids=lambda c: c.name)
+def test_layer_when_the_maximum_moves_far(cfg, low, high, value):
+    """Compressed attention, special tokens and (FIXED) the fixed context."""
+    x = layer_inputs(cfg, low, high, value)
+    res = run_gpu(cfg, x)
+    for h in range(cfg.num_heads):
+        compare_head(cfg, x, res, h)
+
+
+@pytest.mark.parametrize("low,high,value", JUMPS)
+def test_dense_attention_when_the_maximum_moves_far(low, high, value):
+    cfg = WIDE
+    H, F, d = cfg.num_heads, cfg.num_frames, 64
+    x = layer_inputs(cfg, low, high, value)
+    q, k, v = (torch.cat([x[n + "_spec"], x[n + "_img"].reshape(H, F, -1, d)], dim=2).reshape(H, -1, d).contiguous()
+               for n in "qkv")
+    layer = gsa.GSALayer.from_workload(cfg)
+    o = layer.dense(q, k, v)
+    torch.cuda.synchronize()
+    status = layer.status()
+    layer.close()
+    assert status == 0
+    for h in range(H):
+        want = oracle.dense_attention(to_f64_numpy(q[h]), to_f64_numpy(k[h]), to_f64_numpy(v[h]))
+        assert_close("dense", o[h].float().cpu().numpy(), want, cfg)
