@@ -163,8 +163,8 @@ __device__ __forceinline__ float row_max(const uint32_t* v) {
 // the nearest integer, r in [-1/2, 1/2] (Cody and Waite's reduction, exact here), 2^r by
 // the degree-4 polynomial of least relative error (2.6e-6 = 2^-18.6, fitted by Remez'
 // exchange; bf16 weights keep 2^-8, their fp32 sum 2^-18).  Adding 1.5 * 2^23 + 127 leaves
-// n + 127 in the low bits, so one shift gives the float 2^n.  x is held above -126 (2^-126
-// instead of less, or of 0 for -inf: only unmasked tiles come here); NaN stays NaN.
+// n + 127 in the low bits, so one shift gives the float 2^n.  x is held above -127, whose 2^n
+// is 0: less than 2^-126.5, and -inf, give 0 as the exponential unit does; NaN stays NaN.
 __device__ __forceinline__ void exp2_pair_fma(uint32_t s0, uint32_t s1, float sl2, float nmb, float& l0, float& l1,
                                               float& p0, float& p1) {
   float x0, x1;
@@ -173,8 +173,8 @@ __device__ __forceinline__ void exp2_pair_fma(uint32_t s0, uint32_t s1, float sl
       " fma.rn.f32x2 d, a, b, c;\n mov.b64 {%0, %1}, d;\n}\n"
       : "=f"(x0), "=f"(x1)
       : "r"(s0), "r"(s1), "f"(sl2), "f"(nmb));
-  asm("max.NaN.f32 %0, %0, 0fC2FC0000;\n" : "+f"(x0));      // -126
-  asm("max.NaN.f32 %0, %0, 0fC2FC0000;\n" : "+f"(x1));
+  asm("max.NaN.f32 %0, %0, 0fC2FE0000;\n" : "+f"(x0));      // -127
+  asm("max.NaN.f32 %0, %0, 0fC2FE0000;\n" : "+f"(x1));
   constexpr float MAGIC = 12583039.f;                       // 1.5 * 2^23 + 127
   asm("{\n .reg .b64 x, t, r, p, c, m;\n .reg .b32 t0, t1;\n"
       " mov.b64 x, {%0, %1};\n mov.b64 m, {%4, %4};\n add.rn.f32x2 t, x, m;\n"

@@ -68,6 +68,26 @@ def test_cache_attention_when_the_maximum_moves_far(n, hk, group, dtype, rows, s
     clean()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("n,group", [(1, 1), (9, 2), (50, 1), (300, 1)])
+def test_cache_attention_weights_that_are_zero(n, group, dtype):
+    """Scores of -inf throughout a sequence: 0 and -inf, as for a query without a key.  Keys whose weight underflows
+    (2^-432 of the largest) add nothing, however large their values are: 2^126, of which 2^-126 would be one a key."""
+    dt, lengths = TYPES[dtype], [900, 700]
+    s = Streams([n, n], [t - n for t in lengths], 64, 1, dt, seed=n)
+    k0, v0 = keys_and_values(s.g, lengths[0], 1, FALLING, dt)
+    k0[:, 0, 0] = float("-inf")
+    k1, v1 = keys_and_values(s.g, lengths[1], 1, ((0.5, 1.0), (400, -800)), dt)
+    v1[350:] = 2.0 ** 126
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    s.cache.append(torch.cat([k0, k1]), torch.cat([v0, v1]), s.table, i32([0, 0]), i32([0, lengths[0], sum(lengths)]))
+    q = torch.ones(2 * n, group, 64, device="cuda", dtype=dt)
+    out, lse = s.cache.attention(q, s.table, s.lengths, s.cu, n, max_len=1, causal=False, return_lse=True)
+    check_attention(s, q, out, lse, False)
+    assert (out[:n] == 0).all() and (lse[:, :n] == float("-inf")).all()
+    clean()
+
+
 # ---- the layer's kernels --------------------------------------------------------------------
 WIDE = GSAConfig("wide_bf16", 6, 24, 24, 24, 24, 5, 2, 64, 4, 32, "bf16")      # R = 216 regions: two key tiles
 FIXED = GSAConfig("wide_fixed_bf16", 6, 24, 24, 24, 24, 5, 2, 64, 4, 16, "bf16", (0, 4))
