@@ -104,7 +104,7 @@ def algorithmic_work(cfg, kc):
 
 # the sources each timed kernel is compiled from (a traffic record is used only while
 # the hash of its kernel's sources matches the one recorded with it)
-_ATTN_SRC = ("attn_tc.cu", "tc_ptx.cuh", "gsa_common.cuh", "gsa_kernels.h")
+_ATTN_SRC = ("attn_tc.cu", "tc_softmax.cuh", "tc_ptx.cuh", "gsa_common.cuh", "gsa_kernels.h")
 KERNEL_SOURCES = {
     "comp_attn_topk": _ATTN_SRC, "special": _ATTN_SRC, "fixed_attn": _ATTN_SRC, "dense": _ATTN_SRC,
     "selection_gate": ("select.cu", "sel_tc.cu", "tc_ptx.cuh", "gsa_common.cuh", "gsa_kernels.h"),

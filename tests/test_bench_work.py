@@ -69,3 +69,19 @@ def test_traffic_record_is_tied_to_the_sources(tmp_path, monkeypatch):
 def test_each_kernel_hashes_its_own_sources():
     assert bench.kernel_source_sha("pool") != bench.kernel_source_sha("comp_attn_topk")
     assert bench.kernel_source_sha("special") == bench.kernel_source_sha("comp_attn_topk")
+
+
+def test_attention_hash_covers_the_included_headers():
+    """A record of DRAM traffic is dropped when any file that the attention kernels are compiled from changes."""
+    import os
+    import re
+    csrc = os.path.join(bench.ROOT, "sparse_global_attention_b200", "csrc")
+    seen, todo = set(), ["attn_tc.cu"]
+    while todo:
+        name = todo.pop()
+        if name not in seen:
+            seen.add(name)
+            with open(os.path.join(csrc, name)) as f:
+                todo += re.findall(r'#include "([^"/]+)"', f.read())
+    for kernel in ("comp_attn_topk", "special", "fixed_attn", "dense"):
+        assert seen <= set(bench.KERNEL_SOURCES[kernel])
