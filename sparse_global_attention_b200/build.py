@@ -41,17 +41,21 @@ def build_binding() -> str:
     """Compile the binding; ImportError where torch (or what its extension tools need) is not installed."""
     import sysconfig
 
+    import torch
     from torch.utils import cpp_extension
     inc = [*cpp_extension.include_paths(), sysconfig.get_paths()["include"],
            os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")]
     libs = cpp_extension.library_paths()
     tmp = BINDING + ".tmp"
-    cmd = [shutil.which("g++") or "g++", "-std=c++17", "-O2", "-fPIC", "-shared", "-fvisibility=hidden", "-w",
-           *[f"-I{d}" for d in inc], os.path.join(CSRC, "torch_binding.cpp"), "-o", tmp,
+    cmd = [shutil.which("g++") or "g++", "-std=c++17", "-O2", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *[a for d in inc for a in ("-isystem", d)], os.path.join(CSRC, "torch_binding.cpp"), "-o", tmp,
            *[f"-L{d}" for d in libs], "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch", "-ltorch_python"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on torch_binding.cpp:\n{r.stdout}\n{r.stderr}")
+    if r.stderr:
+        sys.stderr.write(r.stderr)
     os.replace(tmp, BINDING)
     return BINDING
 

@@ -5,6 +5,8 @@ import sys
 
 import pytest
 
+from sparse_global_attention_b200 import build as b
+
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 RUN = """
 import sys
@@ -35,3 +37,20 @@ def test_binding_that_does_not_compile_leaves_the_library(tmp_path):
     r = run(tmp_path, "")
     assert r.returncode != 0 and "g++ failed on torch_binding.cpp" in r.stderr
     assert (tmp_path / "lib.so").exists() and not (tmp_path / "binding.so").exists()
+
+
+def test_binding_takes_the_string_type_of_the_installed_torch(tmp_path, monkeypatch):
+    """std::string has two forms in GCC's library; torch's build says which one its symbols take."""
+    import torch
+    seen = []
+
+    def fake(cmd, **kw):
+        seen.append(cmd)
+        open(cmd[cmd.index("-o") + 1], "w").close()
+        return subprocess.CompletedProcess(cmd, 0, "", "")
+    monkeypatch.setattr(b, "BINDING", str(tmp_path / "binding.so"))
+    monkeypatch.setattr(b.subprocess, "run", fake)
+    for abi in (True, False):
+        monkeypatch.setattr(torch._C, "_GLIBCXX_USE_CXX11_ABI", abi)
+        b.build_binding()
+        assert f"-D_GLIBCXX_USE_CXX11_ABI={int(abi)}" in seen[-1]
