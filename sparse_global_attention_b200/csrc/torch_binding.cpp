@@ -216,6 +216,12 @@ at::Tensor item(PyObject* out, Py_ssize_t i, const char* name) {
   return t ? *t : at::Tensor();
 }
 
+// A tensor of the caller's that a call has written (through its pointer): autograd and every other holder of a saved
+// tensor learn of it by the version.  Tensors made in inference mode have none.
+void written(const at::Tensor& t) {
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 PyObject* wrap(const at::Tensor& t) {
   if (t.defined()) return THPVariable_Wrap(t);
   Py_RETURN_NONE;
@@ -286,6 +292,8 @@ PyObject* norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
                           affine(tensor(a[7], "k_weight"), "k_weight", type, dev),
                           affine(tensor(a[8], "k_bias"), "k_bias", type, dev), p.p, p.so, on.stream),
           "gsa_qk_norm_rope");
+    for (int i = 0; i < 3; ++i)
+      if (in[i] && !want[i]) written(res[i]);
     PyObject* t = PyTuple_New(3);
     for (int i = 0; i < 3; ++i) PyTuple_SET_ITEM(t, i, wrap(res[i]));
     return t;
@@ -363,6 +371,8 @@ PyObject* norm_rope_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
                                    affine(tensor(a[9], "k_weight"), "k_weight", type, dev), p.p, p.so, ps[0], ps[1],
                                    ps[2], ps[3], normed ? ws.data_ptr() : nullptr, bytes, on.stream),
           "gsa_qk_norm_rope_backward");
+    for (int i = 0; i < 3; ++i)
+      if (g[i] && !want[i]) written(res[i]);
     static const char* keys[7] = {"dq", "dk", "dv", "dq_weight", "dq_bias", "dk_weight", "dk_bias"};
     PyObject* d = PyDict_New();
     for (int i = 0; i < 7; ++i) {
@@ -430,6 +440,8 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
                        affine(tensor(a[9], "k_weight"), "k_weight", type, dev),
                        affine(tensor(a[10], "k_bias"), "k_bias", type, dev), p.p, on.stream),
           "gsa_cache_append");
+    written(kp);
+    written(vp);
     Py_RETURN_NONE;
   });
 }
@@ -449,8 +461,8 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int max_new = small(a[6], "max_new");
     const int64_t max_len = a[7] == Py_None ? static_cast<int64_t>(c.max_pages) * c.page_size : integer(a[7], "max_len");
     at::Tensor out, lse, ws;
-    if (const at::Tensor* o = tensor(a[11], "out")) out = *o;
-    else out = make({tokens, q.size(1), DIM}, type, dev);
+    const at::Tensor* to = tensor(a[11], "out");
+    out = to ? *to : make({tokens, q.size(1), DIM}, type, dev);
     const gsa_rows ro = rows3(&out, "out", type, dev, &q);
     if (truth(a[10], "return_lse")) lse = make({q.size(1), tokens}, at::kFloat, dev);
     const size_t bytes = g_lib.attention_bytes(&c, tokens, rq.heads, max_new, max_len);
@@ -461,6 +473,7 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
                           lse.defined() ? lse.data_ptr<float>() : nullptr, bytes ? ws.data_ptr() : nullptr, bytes,
                           on.stream),
           "gsa_cache_attention");
+    if (to) written(out);
     if (!lse.defined()) return wrap(out);
     PyObject* t = PyTuple_New(2);
     PyTuple_SET_ITEM(t, 0, wrap(out));
