@@ -14,6 +14,8 @@
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
+#include <torch/csrc/autograd/functions/basic_ops.h>
+#include <torch/csrc/autograd/functions/utils.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <array>
@@ -222,6 +224,29 @@ void written(const at::Tensor& t) {
   if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
 }
 
+// No call records a gradient.  Where autograd would (grad mode, and an argument that requires one), a result that the
+// call makes says so when a gradient is asked of it; the caller's own memory cannot, and is not written.
+bool requires_grad(const at::Tensor* t) { return t && t->requires_grad(); }
+template <typename... T>
+bool recorded(const T*... t) {
+  return at::GradMode::is_enabled() && (requires_grad(t) || ...);
+}
+constexpr const char* UNRECORDED = "call it under torch.no_grad() or with detached tensors";
+void no_history(const char* op, const char* what) {
+  refuse(op, " records no gradient and would write ", what, " with values that require one: ", UNRECORDED);
+}
+// the results `res` depend on `t`
+template <typename... T>
+void no_gradient(const char* op, const char* instead, std::initializer_list<at::Tensor> res, const T*... t) {
+  torch::autograd::edge_list edges;
+  for (const at::Tensor* x : {t...})
+    if (requires_grad(x)) edges.push_back(torch::autograd::impl::gradient_edge(*x));
+  auto node = std::make_shared<torch::autograd::Error>(
+      std::string(op) + " records no gradient: " + instead + UNRECORDED, std::move(edges));
+  for (const at::Tensor& r : res)
+    if (r.defined()) torch::autograd::set_history(r, node);
+}
+
 PyObject* wrap(const at::Tensor& t) {
   if (t.defined()) return THPVariable_Wrap(t);
   Py_RETURN_NONE;
@@ -276,6 +301,10 @@ PyObject* norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
       res[i] = item(a[12], i, outs[i]);
       want[i] = !res[i].defined();
     }
+    const at::Tensor* w[3] = {tensor(a[5], "q_weight"), tensor(a[7], "k_weight"), nullptr};
+    const at::Tensor* b[3] = {tensor(a[6], "q_bias"), tensor(a[8], "k_bias"), nullptr};
+    for (int i = 0; i < 3; ++i)
+      if (in[i] && !want[i] && recorded(in[i], w[i], b[i], &res[i])) no_history("qk_norm_rope", outs[i]);
     make_outputs(res, want, heads, s.outer, s.tokens, head_major, type, dev);
     for (int i = 0; i < 3; ++i) {
       if (!in[i]) continue;
@@ -287,13 +316,15 @@ PyObject* norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const gsa_norm_rope op{gsa_type(type), small(a[3], "norm"), static_cast<float>(number(a[4], "eps")), p.axes,
                            number(a[10], "rope_base")};
     check(g_lib.norm_rope(&op, s.outer, s.tokens, pi[0], pi[1], pi[2], po[0], po[1], po[2],
-                          affine(tensor(a[5], "q_weight"), "q_weight", type, dev),
-                          affine(tensor(a[6], "q_bias"), "q_bias", type, dev),
-                          affine(tensor(a[7], "k_weight"), "k_weight", type, dev),
-                          affine(tensor(a[8], "k_bias"), "k_bias", type, dev), p.p, p.so, on.stream),
+                          affine(w[0], "q_weight", type, dev), affine(b[0], "q_bias", type, dev),
+                          affine(w[1], "k_weight", type, dev), affine(b[1], "k_bias", type, dev), p.p, p.so, on.stream),
           "gsa_qk_norm_rope");
-    for (int i = 0; i < 3; ++i)
-      if (in[i] && !want[i]) written(res[i]);
+    for (int i = 0; i < 3; ++i) {
+      if (!in[i]) continue;
+      if (!want[i]) written(res[i]);
+      else if (recorded(in[i], w[i], b[i]))
+        no_gradient("qk_norm_rope", "its gradients are those of qk_norm_rope_backward; ", {res[i]}, in[i], w[i], b[i]);
+    }
     PyObject* t = PyTuple_New(3);
     for (int i = 0; i < 3; ++i) PyTuple_SET_ITEM(t, i, wrap(res[i]));
     return t;
@@ -426,7 +457,9 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     On on(dev, a[14]);
     const gsa_kv_cache c = cache_of(kp, vp, given(a[4], "block_table"));
     const at::Tensor& k = given(a[2], "k");
-    const gsa_rows rk = rows3(&k, "k", type, dev, nullptr), rv = rows3(tensor(a[3], "v"), "v", type, dev, &k);
+    const at::Tensor *v = tensor(a[3], "v"), *w = tensor(a[9], "k_weight"), *b = tensor(a[10], "k_bias");
+    const gsa_rows rk = rows3(&k, "k", type, dev, nullptr), rv = rows3(v, "v", type, dev, &k);
+    if (recorded(&k, v, w, b, &kp, &vp)) no_history("KVCache.append", "the cache");
     Shape s;
     s.outer = 1;
     s.tokens = k.size(0);
@@ -437,8 +470,7 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
                            number(a[13], "rope_base")};
     check(g_lib.append(&c, &op, s.tokens, &rk, &rv, ints(tensor(a[6], "cu_tokens"), "cu_tokens", c.batch + 1ll, dev),
                        ints(tensor(a[5], "start"), "start", c.batch, dev),
-                       affine(tensor(a[9], "k_weight"), "k_weight", type, dev),
-                       affine(tensor(a[10], "k_bias"), "k_bias", type, dev), p.p, on.stream),
+                       affine(w, "k_weight", type, dev), affine(b, "k_bias", type, dev), p.p, on.stream),
           "gsa_cache_append");
     written(kp);
     written(vp);
@@ -462,6 +494,7 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t max_len = a[7] == Py_None ? static_cast<int64_t>(c.max_pages) * c.page_size : integer(a[7], "max_len");
     at::Tensor out, lse, ws;
     const at::Tensor* to = tensor(a[11], "out");
+    if (to && recorded(&q, &kp, &vp, to)) no_history("KVCache.attention", "out");
     out = to ? *to : make({tokens, q.size(1), DIM}, type, dev);
     const gsa_rows ro = rows3(&out, "out", type, dev, &q);
     if (truth(a[10], "return_lse")) lse = make({q.size(1), tokens}, at::kFloat, dev);
@@ -474,6 +507,7 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
                           on.stream),
           "gsa_cache_attention");
     if (to) written(out);
+    else if (recorded(&q, &kp, &vp)) no_gradient("KVCache.attention", "", {out, lse}, &q, &kp, &vp);
     if (!lse.defined()) return wrap(out);
     PyObject* t = PyTuple_New(2);
     PyTuple_SET_ITEM(t, 0, wrap(out));

@@ -7,7 +7,10 @@ Like GSALayer these pass torch tensors' pointers to the C entry points
 kernels.  Calls go to the current stream of the tensors' device, or to `stream`
 (a raw handle).  Outputs and workspaces are allocated for that stream, one per
 call, so that calls in flight and captured graphs share none.  There is no
-autograd: gradients are calls of their own.  What the device finds wrong
+autograd: gradients are calls of their own, which record none themselves.  In grad
+mode a result of inputs that require a gradient raises when one is asked of it, and
+values that require one are not written to `out` or into a cache (GSAError: use
+torch.no_grad() or detached tensors).  What the device finds wrong
 (a page outside the pool, a place without a page) is reported by
 operator_status().
 """
