@@ -409,7 +409,7 @@ GSA_API int gsa_cache_append(const gsa_kv_cache *cache, const gsa_norm_rope *op,
  *   max_new   : at least the most new tokens of a sequence (one that has more is
  *               left out and recorded); max_new * q heads / kv_heads up to 65535 * 64
  *   max_len   : about the longest of `lengths`; it only sets how the work is split
- *   softmax_scale : 0 for 1 / 8
+ *   softmax_scale : 0 for 1 / 8; its product with log2(e) has to be finite
  *   lse       : optional float32 [q heads][n_tokens], log-sum-exp of the scaled scores;
  *               written where out is
  *   workspace : gsa_cache_attention_workspace_bytes() of the same sizes

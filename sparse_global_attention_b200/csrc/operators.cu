@@ -323,7 +323,7 @@ extern "C" int gsa_cache_attention(const gsa_kv_cache* cache, int64_t n_tokens, 
   GSA_TRY(check_rows(q, cache->dtype, 1, n_tokens, false));
   GSA_TRY(check_rows(out, cache->dtype, 1, n_tokens, true));
   if (out->heads != q->heads) return GSA_ERR_SHAPE;
-  if (!(softmax_scale >= 0.f) || isinf(softmax_scale)) return GSA_ERR_INVALID_ARG;
+  if (!(softmax_scale >= 0.f) || isinf(softmax_scale * LOG2E)) return GSA_ERR_INVALID_ARG;
   if (n_tokens == 0 || cache->batch == 0 || max_new == 0) return GSA_OK;
   if (!cu_tokens || !lengths || !aligned4(cu_tokens) || !aligned4(lengths) || !aligned4(lse)) return GSA_ERR_INVALID_ARG;
   const bool fp32 = cache->dtype == GSA_FP32;

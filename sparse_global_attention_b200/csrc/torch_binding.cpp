@@ -498,11 +498,14 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     out = to ? *to : make({tokens, q.size(1), DIM}, type, dev);
     const gsa_rows ro = rows3(&out, "out", type, dev, &q);
     if (truth(a[10], "return_lse")) lse = make({q.size(1), tokens}, at::kFloat, dev);
+    const double given_scale = number(a[9], "softmax_scale");
+    const float scale = static_cast<float>(given_scale);
+    if (given_scale != 0.0 && scale == 0.f) refuse("softmax_scale is 0 in 32 bits, which stands for 1 / 8: ", given_scale);
     const size_t bytes = g_lib.attention_bytes(&c, tokens, rq.heads, max_new, max_len);
     if (bytes) ws = make({static_cast<int64_t>(bytes)}, at::kByte, dev);
     check(g_lib.attention(&c, tokens, &rq, &ro, ints(tensor(a[5], "cu_tokens"), "cu_tokens", c.batch + 1ll, dev),
                           ints(tensor(a[4], "lengths"), "lengths", c.batch, dev), max_new, max_len,
-                          truth(a[8], "causal"), static_cast<float>(number(a[9], "softmax_scale")),
+                          truth(a[8], "causal"), scale,
                           lse.defined() ? lse.data_ptr<float>() : nullptr, bytes ? ws.data_ptr() : nullptr, bytes,
                           on.stream),
           "gsa_cache_attention");

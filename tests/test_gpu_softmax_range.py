@@ -88,6 +88,22 @@ def test_cache_attention_weights_that_are_zero(n, group, dtype):
     clean()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("n", [1, 50, 300])
+def test_cache_attention_with_scales_at_the_ends(n, dtype):
+    """A scale so small that all keys weigh the same, and one that 32 bits would hold as 0, which stands for 1 / 8."""
+    s = Streams([n], [700 - n], 16, 1, TYPES[dtype], seed=n)
+    s.cache.append(s.rand(n, 1), s.rand(n, 1), s.table, s.start, s.cu)
+    q = s.rand(n, 1)
+    for scale in (1e-40, 1e-30):
+        out, lse = s.cache.attention(q, s.table, s.lengths, s.cu, n, softmax_scale=scale, return_lse=True)
+        check_attention(s, q, out, lse, True, scale=scale)
+    for scale in (1e-60, 2.4e38, 1e39, float("nan")):
+        with pytest.raises(gsa.GSAError):
+            s.cache.attention(q, s.table, s.lengths, s.cu, n, softmax_scale=scale)
+    clean()
+
+
 # ---- the layer's kernels --------------------------------------------------------------------
 WIDE = GSAConfig("wide_bf16", 6, 24, 24, 24, 24, 5, 2, 64, 4, 32, "bf16")      # R = 216 regions: two key tiles
 FIXED = GSAConfig("wide_fixed_bf16", 6, 24, 24, 24, 24, 5, 2, 64, 4, 16, "bf16", (0, 4))

@@ -154,6 +154,13 @@ def test_arrays_of_32_bits_are_aligned(call):
     assert call() == 1
 
 
+def test_softmax_scale_in_units_of_log2():
+    """The kernels take the scale times log2(e), in 32 bits."""
+    none = dict(tokens=0, q=_rows(0, heads=4), out=_rows(0, heads=4))
+    assert _attention(scale=2.4e38, **none) == 1 and _attention(scale=3.4e38, **none) == 1
+    assert _attention(scale=2.3e38, **none) == 0
+
+
 @pytest.mark.parametrize("norm", ["none", "layer", "rms"])
 @pytest.mark.parametrize("axes", [0, 1, 2])
 def test_oracle_gradients_against_differences(norm, axes):
