@@ -326,7 +326,9 @@ typedef struct {
  *   rope_axes 1  channels (i, i + 32), i < 32, turn by p * base^(-i / 32)
  *   rope_axes 2  channels 0..31 turn by the first coordinate, 32..63 by the
  *                second: pairs (i, i + 16) of each half, angle p * base^(-i / 16)
- * Angles are computed in 64 bits; norms and the rotation in fp32, rounded once. */
+ * Angles are computed in 64 bits (with a base of 1 or more off by less than 2^-28 of a
+ * turn at any position; with a smaller base, whose pairs turn faster, in proportion to
+ * the fastest one's turns); norms and the rotation in fp32, rounded once. */
 typedef struct {
     int dtype;          /* GSA_BF16 or GSA_FP32: rows, weights and biases       */
     int norm;           /* GSA_NORM_*                                           */
@@ -413,6 +415,10 @@ GSA_API int gsa_cache_append(const gsa_kv_cache *cache, const gsa_norm_rope *op,
  *   lse       : optional float32 [q heads][n_tokens], log-sum-exp of the scaled scores;
  *               written where out is
  *   workspace : gsa_cache_attention_workspace_bytes() of the same sizes
+ * With GSA_FP32 everything is fp32.  With GSA_BF16 scores, maxima, sums and lse are
+ * fp32; weights are rounded to bf16 for the product with the values (not for their
+ * sum), and in calls with more than 32 rows (max_new times query heads of a key head)
+ * 3 of 16 weights are good to 2^-18.
  * Pages outside the pool are left out as if masked, and recorded.  Memory that no
  * token stands in may hold anything.  A value that is not finite in a token of the
  * sequence can reach every query of it, also those that do not see the token. */

@@ -18,7 +18,7 @@
 // issuer for each stream did not (1183 against 977 us, 1301 queries of 16 heads over 83,264
 // keys, one block per 256 rows), nor turns taken by barriers (1000), three streams
 // of 64-key tiles (1404), or reading the next scores under the exponentials (1464).  (With two
-// warps per 32 rows and the keys split over three blocks the call takes 640 to 660.)  3 of
+// warps per 32 rows and the keys split over three blocks the call takes 670 to 700.)  3 of
 // 16 exponentials run on the FMA pipe (913 against 924 us; 4 of 16: 961).
 // Variants by the rows of a sequence and key head:
 //   ROW_TILES (a chunk of tokens): the streams are two row tiles over the same keys;
@@ -63,7 +63,7 @@ enum Kind : int { ROW_TILES = 0, ONE_TILE = 1, QUARTERS = 2, F32_64 = 3, F32_8 =
 template <int KIND>
 struct Lay {
   static constexpr bool QUAD = KIND == QUARTERS;
-  static constexpr int NS = QUAD ? 1 : 2;                    // streams: four softmax warps and an MMA issuer each
+  static constexpr int NS = QUAD ? 1 : 2;                    // streams: TWARP softmax warps each
   static constexpr int R = KIND == ROW_TILES ? 2 : 1;        // row tiles; with one, stream s takes tiles s, s + NS, ..
   static constexpr int STEP = KIND == ONE_TILE ? NS : 1;
   static constexpr int ROWS = QUAD ? 32 : R * TM;
@@ -241,7 +241,7 @@ __device__ __forceinline__ int row_limit(const CacheAttnArgs& a, const Block& k,
   return a.causal ? min(k.len, max(0, k.seq.len - k.seq.n + token + 1)) : k.len;
 }
 
-// page of slot `t` of sequence b, -1 if the pool has none such
+// an entry of the block table, -1 if the pool has no such page
 __device__ __forceinline__ int page_of(const CacheAttnArgs& a, int raw) {
   return raw >= 0 && raw < a.c.num_pages ? raw : -1;
 }
@@ -578,6 +578,9 @@ __global__ void __launch_bounds__(Lay<KIND>::NTHREADS, KIND == QUARTERS ? 2 : 1)
       }
       const float mb = (m == -INFINITY) ? 0.f : m * sl2;
       float l0 = 0.f, l1 = 0.f;
+      // Weights are rounded to bf16 (half a step is 2^-8) for the product, since both of its operands are
+      // of one type and the values are bf16; their sum takes them in 32 bits.  The error of an output is
+      // that of its own rounding once more: 0.0023 of the result's norm against 0.0016 with exact weights.
       auto weights = [&](auto mixed) {
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
@@ -899,9 +902,10 @@ __global__ void __launch_bounds__(256, 2) cache_attn_f32_kernel(const __grid_con
 // 8 shuffles for 8 keys), so that lane c ends with the score of key 2 (c / (16 / N)) + half; the
 // weights are handed back by shuffles for O += p V.  Each warp has its own running maximum and
 // sums; the block's eight warps are joined at the end.  A step's keys lie in one page.  16 rows by
-// 64 keys through shared memory (one row a thread) read 1.6 TB/s where this reads 5.6 (48
-// sequences of 9728 tokens, single new ones, 4 key heads and 16 query heads: 0.96 GB in 170 us; one
-// query head for each key head 151 us, 6.3 TB/s).
+// 64 keys through shared memory (one row a thread) read 1.6 TB/s where this reads 5.4 (48
+// sequences of 9728 tokens, single new ones, 4 key heads and 16 query heads: 0.96 GB in 175 to 180 us;
+// one query head for each key head 152 us, 6.3 TB/s; eight, in tiles of 8 rows, 371 us, 2.6 TB/s:
+// bound by the rows' products and exchanges).
 template <int R, int N>
 __global__ void __launch_bounds__(256, 2) cache_attn_f32_few_kernel(const __grid_constant__ CacheAttnArgs a) {
   constexpr int KEYS = 2 * N, WARPS = 8, PART = 66;

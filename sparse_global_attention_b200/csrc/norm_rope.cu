@@ -11,8 +11,9 @@
 // registers (the variance from the centred values), everything is fp32 with one rounding
 // at the store.  The 32 angles of a token are computed once and serve all
 // its heads.  An angle is a part of a turn in 64-bit fixed point (position times turns per
-// position modulo 2^64 is one integer product, off by 2^-34 of a turn at the most), so
-// positions far into a stream lose nothing; its upper half goes to sincospif.
+// position modulo 2^64 is one integer product, off by less than 2^-28 of a turn: make_table
+// has the derivation), so positions far into a stream lose nothing; its upper half goes to
+// sincospif, whose argument keeps 2^-26 of a turn.
 //
 // Bound by HBM.  Each warp loads the rows of four heads a lane before it works on them; a grid
 // of what the SMs hold keeps the tokens in flight together, so that the rows of each head are
@@ -172,13 +173,13 @@ struct Turn<0> {
   __device__ __forceinline__ void apply(Lane8&) const {}
 };
 
-// turns per unit of position of this lane's channel pair, in 2^-64
-// of the lane's own four pairs
+// turns per unit of position, in 2^-64, of the lane's own four pairs
 template <int AXES>
 __device__ __forceinline__ void own_freq(const RopeTable& t, int lane, unsigned long long (&f)[4]) {
 #pragma unroll
   for (int e = 0; e < 4; ++e) f[e] = AXES == 0 ? 0 : t.f[(4 * (lane & 7) + e) & (AXES == 2 ? 15 : 31)];
 }
+// and of the pair whose angle this lane computes for the others
 template <int AXES>
 __device__ __forceinline__ unsigned long long lane_freq(const RopeTable& r, int lane) {
   if constexpr (AXES == 0) return 0;

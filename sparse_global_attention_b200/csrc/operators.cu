@@ -81,8 +81,12 @@ int check_op(const gsa_norm_rope* op) {
 }
 
 // Turns per unit of position, base^(-i / half) / (2 pi), modulo a turn in 64-bit fixed point.
-// One power and a product for each next pair (32 powers were 3 us of a call): off by at most
-// 33 roundings of 2^-64, so a position of 2^31 by less than 2^-28 of a turn.
+// One power and a product for each next pair (32 powers were 3 us of a call).  In units of 2^-64
+// relative: the constant and the quotient 1 each, the power 2 (one place of the last), a product
+// 2 + 1, so at most 2 + 31 * 3 = 95.  With a base of 1 or more no frequency is above 1 / (2 pi), so
+// it is off by less than 0.16 * 95 + 1 (the cut to fixed point) < 2^5 units of 2^-64 of a turn, and a
+// position of up to 2^31 by less than 2^-28 of a turn.  With a base below 1 frequencies grow, up to
+// base^-1 / (2 pi) turns, and the error in proportion (still 95 roundings of 2^-64 of the angle).
 void make_table(const gsa_norm_rope* op, RopeTable* t) {
   memset(t, 0, sizeof(*t));
   if (op->rope_axes == 0) return;

@@ -57,7 +57,8 @@ def qk_norm_rope(q, k=None, v=None, *, norm="layer", eps=1e-5, q_weight=None, q_
     may be None.  norm: "layer" (weight, optional bias), "rms" (weight) or "none".  positions: int32 [tokens, axes] or
     [outer, tokens, axes]; one axis turns channels (i, i + 32), two turn the halves by a coordinate each; None: no
     rotation.  head_major: outputs are [heads, outer, tokens, 64], the layer's layout.  out: tensors of the output
-    shapes to write (q, k, v), which may be the inputs themselves.  Returns (q, k, v), None where there was none."""
+    shapes to write (q, k, v), which may be the inputs themselves.  Returns (q, k, v), None where there was none.  Outputs
+    of up to 256 KB together share one allocation: one that is kept (or saved) keeps all; clone it to keep it alone."""
     return _b.norm_rope(q, k, v, _norm(norm), eps, q_weight, q_bias, k_weight, k_bias, positions, rope_base, head_major, out,
                         stream)
 
@@ -69,7 +70,8 @@ def qk_norm_rope_backward(q, k, dq, dk, dv=None, *, norm="layer", eps=1e-5, q_we
 
     Returns {"dq", "dk", "dv"} of the gradients' type, shaped like the inputs [outer, tokens, heads, 64] (or written
     to `out`), and float32 {"dq_weight", "dq_bias", "dk_weight", "dk_bias"}; None where there is none (a bias has a
-    gradient when it is given).  q and k may be None with norm "none"."""
+    gradient when it is given).  q and k may be None with norm "none".  dq, dk and dv of up to 256 KB together share one
+    allocation, and so do the four gradients of weights and biases."""
     return _b.norm_rope_backward(q, k, dq, dk, dv, _norm(norm), eps, q_weight, q_bias, k_weight, k_bias, positions, rope_base,
                                  head_major, out, stream)
 

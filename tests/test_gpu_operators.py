@@ -138,6 +138,18 @@ def test_positions_at_the_ends_of_their_range(axes):
     assert_within("q", f64(q), want, (256 * U + 2.0 ** -18) * big)
 
 
+@pytest.mark.parametrize("axes", [1, 2])
+@pytest.mark.parametrize("base", [1.0, 0.01, 1e-4])
+def test_norm_rope_with_a_base_of_one_or_less(base, axes):
+    """Pairs that turn by up to 1 / base a position: the oracle's own angles, 4000 / base at the most, are off by 2^-53 of
+    that, 2^-27; the kernel's by 95 roundings of 2^-64 of it.  Both below 2^-22, an eighth of the bound's 2^-19."""
+    g = torch.Generator(device="cuda").manual_seed(8)
+    x, w, pos = norm_inputs(g, 2, 70, 3, 1, torch.float32, "rms", axes)
+    q, k, _ = gsa.qk_norm_rope(x["q"], x["k"], norm="rms", eps=1e-5, positions=pos, rope_base=base, **w)
+    check_norm_rope({"q": x["q"], "k": x["k"]}, w, pos, "rms", axes, base, {"q": q, "k": k}, torch.float32, 1e-5)
+    clean()
+
+
 def test_norm_rope_strides_shared_positions_and_parts():
     """A fused projection's views, one set of positions for all frames, outputs into a larger buffer, parts left out."""
     g = torch.Generator(device="cuda").manual_seed(6)
