@@ -393,7 +393,9 @@ typedef struct {
  *   positions : int32 [n_tokens][rope_axes]; NULL with rope_axes 0, and with
  *               rope_axes 1 for a token's own place in its sequence
  * A token whose place has no page in the table, or whose page is not one of the
- * pool, is left out (GSA_ERR_DEVICE_BOUNDS from gsa_operator_status).  Two
+ * pool, is left out (GSA_ERR_DEVICE_BOUNDS from gsa_operator_status); a sequence that
+ * starts before the rows, ends behind them or has a negative length is recorded alike,
+ * and its rows that there are may be written to its pages.  Two
  * tokens with the same place leave either of the two in it. */
 GSA_API int gsa_cache_append(const gsa_kv_cache *cache, const gsa_norm_rope *op, int64_t n_tokens,
                              const gsa_rows *k, const gsa_rows *v, const int32_t *cu_tokens,

@@ -295,6 +295,16 @@ __device__ __forceinline__ long long paged_row_of(const NormRopeArgs& a, long lo
   return place_row(a, lo, t, tell, place);
 }
 
+// What the rows do not show of cu: sequences that start before them, end behind them or have a negative
+// length.  The last block looks, after its own items.
+__device__ __forceinline__ void check_sequences(const NormRopeArgs& a) {
+  if (blockIdx.x != gridDim.x - 1) return;
+  for (int b = threadIdx.x; b < a.c.batch; b += NTHR) {
+    const int first = a.cu[b], end = a.cu[b + 1];
+    if (first < 0 || end < first || end > a.n_tokens) set_error(a.err, ERR_BOUNDS);
+  }
+}
+
 // An item is up to U quads of one token: `left` heads from `head` on.
 struct Item {
   long long o, t;
@@ -386,6 +396,7 @@ __global__ void __launch_bounds__(NTHR, 3) norm_rope_kernel(const __grid_constan
       }
     }
   }
+  if constexpr (PAGED) check_sequences(a);
 }
 
 // Large calls: each group of eight lanes takes a token of its own and goes through its heads four at a
@@ -473,6 +484,7 @@ __global__ void __launch_bounds__(NTHR, 3) norm_rope_group_kernel(const __grid_c
       }
     }
   }
+  if constexpr (PAGED) check_sequences(a);
 }
 
 // Gradients: with g the output gradient turned back and h the normalised row,

@@ -411,6 +411,28 @@ def test_append_leaves_out_what_has_no_page():
     assert len(left) == 8 and np.array_equal(f64(s.cache.k_pages), want, equal_nan=True)
 
 
+@pytest.mark.parametrize("many", [False, True])
+@pytest.mark.parametrize("place,value", [(3, 99), (3, 9000), (0, -2), (2, 1), (1, -5), (4, 0)])
+def test_append_records_wrong_sequences(place, value, many):
+    """cu_tokens that end behind the rows, start before them or decrease: recorded, and no row outside the sequences'
+    own pages is touched."""
+    per = 800 if many else 3
+    s = Streams([per] * 4, [5] * 4, 16, 2, torch.bfloat16)
+    cu = s.cu.clone()
+    cu[place] = value if value != 99 else 4 * per + 1
+    k, v = s.rand(4 * per, 2), s.rand(4 * per, 2)
+    before = s.cache.k_pages.clone()
+    clean()
+    s.cache.append(k, v, s.table, s.start, cu)
+    assert gsa.operator_status() == 7
+    spare = torch.ones(s.cache.num_pages, dtype=torch.bool, device="cuda")
+    spare[s.table[s.table >= 0].long()] = False
+    assert spare.any() and torch.equal(s.cache.k_pages[spare].nan_to_num(7.0), before[spare].nan_to_num(7.0))
+    # rows behind the last sequence are no mistake
+    s.cache.append(s.rand(4 * per + 7, 2), s.rand(4 * per + 7, 2), s.table, s.start, s.cu)
+    clean()
+
+
 # ---- attention over the cache ----------------------------------------------------------------
 def check_attention(s, q, out, lse, causal, scale=0.125, table=None, lengths=None, cu=None):
     table = s.table.cpu().numpy() if table is None else table
