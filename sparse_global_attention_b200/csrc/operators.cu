@@ -328,11 +328,12 @@ extern "C" int gsa_cache_attention(const gsa_kv_cache* cache, int64_t n_tokens, 
   GSA_TRY(check_rows(out, cache->dtype, 1, n_tokens, true));
   if (out->heads != q->heads) return GSA_ERR_SHAPE;
   if (!(softmax_scale >= 0.f) || isinf(softmax_scale * LOG2E)) return GSA_ERR_INVALID_ARG;
-  if (n_tokens == 0 || cache->batch == 0 || max_new == 0) return GSA_OK;
+  if (n_tokens == 0 || cache->batch == 0) return GSA_OK;
   if (!cu_tokens || !lengths || !aligned4(cu_tokens) || !aligned4(lengths) || !aligned4(lse)) return GSA_ERR_INVALID_ARG;
   const bool fp32 = cache->dtype == GSA_FP32;
+  // (with max_new 0 the blocks only look for sequences that have tokens all the same)
   const CacheAttnPlan p =
-      plan_cache_attn(fp32, cache->batch, cache->kv_heads, q->heads, n_tokens, max_new, max_len);
+      plan_cache_attn(fp32, cache->batch, cache->kv_heads, q->heads, n_tokens, max_new, max_new ? max_len : 0);
   if (p.bytes && (!workspace || !aligned16(workspace) || workspace_bytes < p.bytes)) return GSA_ERR_INVALID_ARG;
   int* words = nullptr;
   GSA_TRY(status_words(&words));

@@ -561,6 +561,21 @@ def test_attention_refuses_bad_sequences_on_the_device():
     clean()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_attention_of_no_new_tokens_at_most(dtype):
+    """max_new 0: sequences that have new tokens are left out and recorded, as with any other max_new that is too small."""
+    s = Streams([2, 0, 1], [20, 30, 0], 16, 2, TYPES[dtype], width=3000)
+    q = s.rand(3, 2)
+    clean()
+    for max_len in (None, 0):
+        out = torch.full_like(q, 3.0)
+        s.cache.attention(q, s.table, s.lengths, s.cu, 0, out=out, max_len=max_len, return_lse=True)
+        assert gsa.operator_status() == 7 and (out == 3).all()
+        s.cache.attention(q, s.table, s.lengths, torch.zeros_like(s.cu), 0, out=out, max_len=max_len)
+        clean()
+        assert (out == 3).all()
+
+
 def test_attention_values_of_special_size():
     """Large scores; infinities and NaN in real keys reach the sequence's outputs, and no other's."""
     s = Streams([1, 1, 1], [200, 200, 200], 16, 1, torch.bfloat16)
