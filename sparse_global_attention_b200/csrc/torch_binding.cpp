@@ -227,6 +227,8 @@ void written(const at::Tensor& t) {
 // No call records a gradient.  Where autograd would (grad mode, and an argument that requires one), a result that the
 // call makes says so when a gradient is asked of it; the caller's own memory cannot, and is not written.
 bool requires_grad(const at::Tensor* t) { return t && t->requires_grad(); }
+// a weight or bias that a call with this norm reads
+const at::Tensor* used(int norm, const at::Tensor* t) { return norm == GSA_NORM_NONE ? nullptr : t; }
 template <typename... T>
 bool recorded(const T*... t) {
   return at::GradMode::is_enabled() && (requires_grad(t) || ...);
@@ -301,10 +303,11 @@ PyObject* norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
       res[i] = item(a[12], i, outs[i]);
       want[i] = !res[i].defined();
     }
+    const int norm = small(a[3], "norm");
     const at::Tensor* w[3] = {tensor(a[5], "q_weight"), tensor(a[7], "k_weight"), nullptr};
     const at::Tensor* b[3] = {tensor(a[6], "q_bias"), tensor(a[8], "k_bias"), nullptr};
     for (int i = 0; i < 3; ++i)
-      if (in[i] && !want[i] && recorded(in[i], w[i], b[i], &res[i])) no_history("qk_norm_rope", outs[i]);
+      if (in[i] && !want[i] && recorded(in[i], used(norm, w[i]), used(norm, b[i]), &res[i])) no_history("qk_norm_rope", outs[i]);
     make_outputs(res, want, heads, s.outer, s.tokens, head_major, type, dev);
     for (int i = 0; i < 3; ++i) {
       if (!in[i]) continue;
@@ -313,7 +316,7 @@ PyObject* norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
       po[i] = &ro[i];
     }
     const Positions p = positions(tensor(a[9], "positions"), s, dev);
-    const gsa_norm_rope op{gsa_type(type), small(a[3], "norm"), static_cast<float>(number(a[4], "eps")), p.axes,
+    const gsa_norm_rope op{gsa_type(type), norm, static_cast<float>(number(a[4], "eps")), p.axes,
                            number(a[10], "rope_base")};
     check(g_lib.norm_rope(&op, s.outer, s.tokens, pi[0], pi[1], pi[2], po[0], po[1], po[2],
                           affine(w[0], "q_weight", type, dev), affine(b[0], "q_bias", type, dev),
@@ -322,8 +325,9 @@ PyObject* norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     for (int i = 0; i < 3; ++i) {
       if (!in[i]) continue;
       if (!want[i]) written(res[i]);
-      else if (recorded(in[i], w[i], b[i]))
-        no_gradient("qk_norm_rope", "its gradients are those of qk_norm_rope_backward; ", {res[i]}, in[i], w[i], b[i]);
+      else if (recorded(in[i], used(norm, w[i]), used(norm, b[i])))
+        no_gradient("qk_norm_rope", "its gradients are those of qk_norm_rope_backward; ", {res[i]}, in[i], used(norm, w[i]),
+                    used(norm, b[i]));
     }
     PyObject* t = PyTuple_New(3);
     for (int i = 0; i < 3; ++i) PyTuple_SET_ITEM(t, i, wrap(res[i]));
@@ -459,14 +463,15 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor& k = given(a[2], "k");
     const at::Tensor *v = tensor(a[3], "v"), *w = tensor(a[9], "k_weight"), *b = tensor(a[10], "k_bias");
     const gsa_rows rk = rows3(&k, "k", type, dev, nullptr), rv = rows3(v, "v", type, dev, &k);
-    if (recorded(&k, v, w, b, &kp, &vp)) no_history("KVCache.append", "the cache");
+    const int norm = small(a[7], "norm");
+    if (recorded(&k, v, used(norm, w), used(norm, b), &kp, &vp)) no_history("KVCache.append", "the cache");
     Shape s;
     s.outer = 1;
     s.tokens = k.size(0);
     const Positions p = positions(tensor(a[11], "positions"), s, dev);
     const int axes = small(a[12], "rope_axes");
     if (p.p && p.axes != axes) refuse("positions have ", p.axes, " axes, rope_axes is ", axes);
-    const gsa_norm_rope op{gsa_type(type), small(a[7], "norm"), static_cast<float>(number(a[8], "eps")), axes,
+    const gsa_norm_rope op{gsa_type(type), norm, static_cast<float>(number(a[8], "eps")), axes,
                            number(a[13], "rope_base")};
     check(g_lib.append(&c, &op, s.tokens, &rk, &rv, ints(tensor(a[6], "cu_tokens"), "cu_tokens", c.batch + 1ll, dev),
                        ints(tensor(a[5], "start"), "start", c.batch, dev),

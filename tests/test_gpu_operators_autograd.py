@@ -74,6 +74,12 @@ def test_results_of_inputs_that_require_a_gradient():
             assert not any(t.requires_grad for t in call(**kw))
         with torch.inference_mode():
             assert not any(t.requires_grad for t in call(**kw))
+    # weights that a call without a norm does not read
+    out = rows(2, 9, 4)
+    got = gsa.qk_norm_rope(q, k, norm="none", q_weight=leaf(w), k_weight=leaf(w), out=(out, None, None))
+    assert got[0] is out and not got[1].requires_grad and torch.equal(out, q)
+    s = Streams([3], [5], 16, 2, torch.float32)
+    s.cache.append(rows(3, 2), rows(3, 2), s.table, s.start, s.cu, norm="none", k_weight=leaf(w))
     # the gradients' call takes such tensors and records nothing itself
     r = gsa.qk_norm_rope_backward(leaf(q), None, rows(2, 9, 4), None, norm="rms", q_weight=leaf(w))
     assert not r["dq"].requires_grad and not r["dq_weight"].requires_grad
